@@ -33,6 +33,11 @@ zero outside the grid.  Entry points mirror ``include/hyenand.h``:
   forward in one call
 * ``fftconv_fwd_noalloc(...)`` -- the forward with the library's static
   workspace (for callers that cannot allocate)
+* ``block_norm``, ``block_join``, ``dropout``, ``gated_ffn`` -- the residual
+  block around the convolution, differentiable, on the same [B, C, *dims]
+  layout (``block.py``: the norm ahead of a block, the join behind it, dropout
+  without a stored mask, the gated feed-forward block), with their ``_fwd`` and
+  ``_bwd`` calls
 
 Calls without a ``workspace`` argument take one from a cache keyed by kind,
 device, size and stream; ``release_workspaces()`` frees it.
@@ -64,7 +69,11 @@ EXPORTS = ("hyenand_status_string", "hyenand_version", "hyenand_kernel_spectrum_
            "hyenand_fftconv_bwd_per_sample_traced", "hyenand_generate_workspace_bytes",
            "hyenand_generate_kernel_spectrum", "hyenand_fftconv_fwd_noalloc",
            "hyenand_fftconv_fwd_noalloc_max_workspace", "hyenand_fftconv_fwd_generated",
-           "hyenand_fftconv_fwd_generated_workspace_bytes", "hyenand_fftconv_fwd_generated_workspace_min_bytes")
+           "hyenand_fftconv_fwd_generated_workspace_bytes", "hyenand_fftconv_fwd_generated_workspace_min_bytes",
+           "hyenand_block_norm_fwd", "hyenand_block_norm_bwd_workspace_bytes", "hyenand_block_norm_bwd",
+           "hyenand_block_join_fwd", "hyenand_block_join_bwd_workspace_bytes", "hyenand_block_join_bwd",
+           "hyenand_dropout", "hyenand_gated_ffn_workspace_bytes", "hyenand_gated_ffn_bwd_workspace_bytes",
+           "hyenand_gated_ffn_fwd", "hyenand_gated_ffn_bwd")
 
 _lib = None
 
@@ -162,6 +171,7 @@ def get_lib() -> ctypes.CDLL:
     lib.hyenand_fftconv_fwd_generated_workspace_bytes.restype = SZ
     lib.hyenand_fftconv_fwd_generated_workspace_min_bytes.argtypes = [I, I, I, P, I]
     lib.hyenand_fftconv_fwd_generated_workspace_min_bytes.restype = SZ
+    block._declare(lib)
     _lib = lib
     return lib
 
@@ -822,3 +832,10 @@ def fftconv_fwd_generated(x: torch.Tensor, alpha: torch.Tensor, beta: torch.Tens
     if rc != OK:
         raise HyenandError(rc, "fftconv_fwd_generated")
     return y, K_hat
+
+
+from . import block  # noqa: E402  (the block's operators use the helpers above)
+from .block import (BlockJoinFunction, BlockNormFunction, DropoutFunction, GatedFFNFunction,  # noqa: E402,F401
+                    block_join, block_join_bwd, block_join_fwd, block_norm, block_norm_bwd, block_norm_fwd, dropout,
+                    dropout_bwd, dropout_fwd, gated_ffn, gated_ffn_bwd, gated_ffn_bwd_workspace_bytes, gated_ffn_fwd,
+                    gated_ffn_workspace_bytes)

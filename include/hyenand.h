@@ -404,6 +404,150 @@ size_t hyenand_fftconv_fwd_noalloc_max_workspace(void);
 int hyenand_fftconv_fwd_noalloc(const void* x, const float* phi_alpha, const float* phi_beta, const void* K_hat,
                                 void* y, int B, int C, int d, const int64_t* dims, int dtype, void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The residual block around the convolution.  A layer of a HyenaND stack is
+ *
+ *     h = norm(x);  m = mixer(h);  out = x + scale * gate * norm(m);  h' = norm(out)
+ *
+ * followed by the same with a feed-forward block in the mixer's place.  The
+ * entry points below compute what stands around the mixer on the mixer's own
+ * layout, [B][C][dims]: sums over channels run per batch entry and position.
+ * The conventions at the top hold with these differences:
+ *   - Every extent >= 0 is supported (d in {1, 2, 3}, no power of two needed);
+ *     an extent of zero is an empty call.  Gradients of parameters over an empty
+ *     batch or grid are written as zeros.
+ *   - Statistics, products and sums are fp32 (the sums of parameter gradients
+ *     are joined in double, in a fixed order: bit-identical from call to call);
+ *     results round once to the tensors' dtype, to nearest even.
+ *   - Outputs must not alias inputs or each other.
+ */
+
+/* Activations. */
+#define HYENAND_ACT_NONE 0    /* a(v) = v            (join's gate)                      */
+#define HYENAND_ACT_SIGMOID 1 /* 1 / (1 + exp(-v))   (join's gate, feed-forward)        */
+#define HYENAND_ACT_SILU 2    /* v / (1 + exp(-v))   (join's gate, feed-forward)        */
+#define HYENAND_ACT_GELU 3    /* v Phi(v), Phi the normal distribution (feed-forward)   */
+
+/*
+ * The norm ahead of a block, over the channels:
+ *     r[b,i] = (mean_c x[b,c,i]^2 + eps)^(-1/2),   h[b,c,i] = x[b,c,i] r[b,i] w[c].
+ * x, h: device [B][C][dims] of `dtype`; w: device fp32 [C]; eps > 0, finite.
+ * C <= 8192 (else UNSUPPORTED).  No workspace.
+ * Errors: INVALID_ARG, UNSUPPORTED, HIP.
+ */
+int hyenand_block_norm_fwd(const void* x, const float* w, void* h, int B, int C, int d, const int64_t* dims, int dtype,
+                           float eps, void* stream);
+/*
+ * Its backward for dh = dLoss/dh, with n = dh w:
+ *     dx = r n - x r^3 mean_c(n x),   dw_c = sum_{b,i} dh x r.
+ * dw: device fp32 [C].  workspace: device scratch of the queried size (4-byte
+ * aligned), contents unspecified on entry and exit.  Errors as above, and
+ * WORKSPACE.
+ */
+size_t hyenand_block_norm_bwd_workspace_bytes(int B, int C, int d, const int64_t* dims, int dtype);
+int hyenand_block_norm_bwd(const void* x, const float* w, const void* dh, void* dx, float* dw, int B, int C, int d,
+                           const int64_t* dims, int dtype, float eps, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/*
+ * The join behind a block, in one pass over the tensors: the norm of the
+ * block's output m, its gate and residual scale, dropout, the residual sum and
+ * the next block's norm:
+ *     n   = m r_m w_post          r_m = (mean_c m^2 + eps)^(-1/2)   (n = m where w_post is NULL)
+ *     b   = scale_c a(gate) n     (scale, gate: 1 where NULL)
+ *     out = x + keep b / (1 - p)  (keep: see hyenand_dropout, on b's linear index in [B][C][dims])
+ *     h   = out r_o w_pre         r_o = (mean_c out^2 + eps)^(-1/2) (not computed where w_pre is NULL)
+ * h uses the unrounded out.  A dropped element passes x through, whatever b
+ * holds there.
+ * gate: device [B][C][dims] of `dtype`; gate_act: HYENAND_ACT_NONE, _SIGMOID or
+ * _SILU; scale, w_post, w_pre: device fp32 [C]; p in [0, 1); rng: device, two
+ * 64-bit words {seed, offset}, 8-byte aligned (unused for p = 0).  Pointers may
+ * be NULL as stated.  C <= 8192 (else UNSUPPORTED).
+ */
+typedef struct hyenand_join {
+    const void* gate;
+    const float* scale;
+    const float* w_post;
+    const float* w_pre;
+    const uint64_t* rng;
+    double p;
+    float eps;
+    int gate_act;
+} hyenand_join;
+/* h must be NULL exactly where j->w_pre is.  Errors: INVALID_ARG, UNSUPPORTED, HIP. */
+int hyenand_block_join_fwd(const void* x, const void* m, const hyenand_join* j, void* out, void* h, int B, int C,
+                           int d, const int64_t* dims, int dtype, void* stream);
+/*
+ * Its backward, for dout = dLoss/dout and dh = dLoss/dh (either may be NULL:
+ * zero; dh must be NULL where w_pre is).  Everything between is recomputed from
+ * x, m, gate and the generator's words, which must be those of the forward:
+ *     do  = dout + (the norm's backward of dh at out)
+ *     dx  = do,   db = keep do / (1 - p),   dgate = db scale n a'(gate)
+ *     dscale_c = sum db a n,   dm, dw_post = (the norm's backward of db scale a at m)
+ *     dw_pre_c = sum dh out r_o
+ * grads: dx, dm [B][C][dims] of `dtype`; dgate likewise, NULL exactly where the
+ * gate is; dscale, dw_post, dw_pre fp32 [C], each NULL exactly where its input
+ * is.  workspace as for hyenand_block_norm_bwd.
+ */
+typedef struct hyenand_join_grads {
+    void* dx;
+    void* dm;
+    void* dgate;
+    float* dscale;
+    float* dw_post;
+    float* dw_pre;
+} hyenand_join_grads;
+size_t hyenand_block_join_bwd_workspace_bytes(int B, int C, int d, const int64_t* dims, int dtype);
+int hyenand_block_join_bwd(const void* x, const void* m, const hyenand_join* j, const void* dout, const void* dh,
+                           const hyenand_join_grads* grads, int B, int C, int d, const int64_t* dims, int dtype,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Dropout whose mask is never stored: element e of n is kept iff
+ *     word(e) >= floor(p 2^32),   word(e) = Philox4x32-10(counter = offset + e / 4, key = seed)[e % 4]
+ * (Salmon et al., "Parallel random numbers: as easy as 1, 2, 3", 2011: counter
+ * words {low, high, 0, 0}, key words {low, high}), and y = x / (1 - p) where
+ * kept (the factor rounded to fp32), else 0.  The backward is the same call on
+ * the gradient with the same {seed, offset}.  rng lives on the device so that a
+ * captured graph draws new masks when the caller advances the offset (by
+ * ceil(n / 4) for words not used before).  x, y: device, n elements of
+ * `dtype`, n <= 2^38 (else UNSUPPORTED); p in [0, 1), rng unused for p = 0.
+ * Errors: INVALID_ARG, UNSUPPORTED, HIP.
+ */
+#define HYENAND_DROPOUT_MAX_ELEMENTS ((int64_t)1 << 38)
+int hyenand_dropout(const void* x, void* y, int64_t n, int dtype, double p, const uint64_t* rng, void* stream);
+
+/*
+ * Gated feed-forward block, per batch entry and position:
+ *     g = Wg x,   u = Wu x,   h = a(g) u,   y = Wd h.
+ * x, y: device [B][C][dims]; Wg, Wu: device [F][C]; Wd: device [C][F], all of
+ * `dtype`, row-major, 16-byte aligned.  act: HYENAND_ACT_SIGMOID, _SILU or
+ * _GELU.  F >= 1; C, F <= 65536 and B prod(dims) <= 2^30 (else UNSUPPORTED).
+ * Products are summed in fp32; for bf16, h (and backward g, u, and their
+ * gradients) round to bf16 between the products.
+ * workspace: device scratch, 256-byte aligned, at least the queried size;
+ * contents unspecified on entry and exit.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, HIP.
+ */
+#define HYENAND_FFN_MAX_WIDTH 65536
+#define HYENAND_FFN_MAX_POSITIONS (1 << 30)
+size_t hyenand_gated_ffn_workspace_bytes(int B, int C, int F, int d, const int64_t* dims, int dtype);
+int hyenand_gated_ffn_fwd(const void* x, const void* Wg, const void* Wu, const void* Wd, void* y, int B, int C, int F,
+                          int d, const int64_t* dims, int dtype, int act, void* workspace, size_t workspace_bytes,
+                          void* stream);
+/*
+ * Its backward for dy = dLoss/dy; g, u and h are recomputed from x:
+ *     dh = Wd^T dy,   du = dh a(g),   dg = dh u a'(g),
+ *     dx = Wg^T dg + Wu^T du,   dWg = sum dg x^T,   dWu = sum du x^T,   dWd = sum dy h^T
+ * (sums over batch entries and positions, in a fixed order).  Every gradient has
+ * the dtype and layout of its input and is overwritten.
+ */
+size_t hyenand_gated_ffn_bwd_workspace_bytes(int B, int C, int F, int d, const int64_t* dims, int dtype);
+int hyenand_gated_ffn_bwd(const void* x, const void* Wg, const void* Wu, const void* Wd, const void* dy, void* dx,
+                          void* dWg, void* dWu, void* dWd, int B, int C, int F, int d, const int64_t* dims, int dtype,
+                          int act, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
