@@ -1,0 +1,391 @@
+// ffn_tile.h -- the matrix-core product of the gated feed-forward block: a
+// workgroup computes one or two row groups of A times one tile of B, with the
+// operation's epilogue on the accumulators.
+//
+// Every operand is a bf16 matrix in rows of 16-byte multiples.  A (weights, or
+// gradients in the weight gradients) has its summation index k contiguous.  B
+// is either k-contiguous too, or (activations of a [channel][position] layout)
+// contiguous along its columns; then the transposing LDS read brings four
+// consecutive k of a column into a lane, so activations are used where they lie.
+//
+// fp32 operands come as three bf16 planes whose sum is the value (8 bits each,
+// split by truncation: exact, and the leading plane cannot overflow).  A product
+// of two such sums runs as six phases over pairs of planes, smallest first,
+// into the same fp32 accumulators; the three pairs left out are below 2^-23 of
+// |a| |b|.  Six bf16 phases have 2.7 times the rate of the fp32 matrix
+// instruction (2.5 / 6 against 0.157 PFLOP/s).
+//
+// Pipeline: two LDS stages of 64 terms.  Loads go from global memory straight
+// to LDS (16 bytes a lane) one stage ahead, so a stage has the whole product of
+// the stage before to arrive; one barrier per stage.
+#pragma once
+
+#include "block_dev.h"
+
+namespace hyenand {
+namespace {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kBK = 64;          // terms of a stage
+constexpr int kMaxPhases = 12;
+
+__device__ __align__(16) const unsigned g_zeros[4] = {0, 0, 0, 0};
+
+// k-contiguous rows: element (r, k) at r * ld + (k / L) * sb + k % L (L: the
+// positions of a batch entry, or more than K for one piece).
+// Column-contiguous (B only): element (k, n) at k * ld + (n / L) * sb + n % L.
+struct Mat {
+    long long ld, sb;
+    int L;
+};
+
+struct TileArgs {
+    // Phase p adds A[p][g] B[p] to row group g of the accumulators; phases from
+    // n1 on (gradient epilogue) to the third group, with K2 terms.
+    const __bf16 *A0[kMaxPhases], *A1[kMaxPhases], *B[kMaxPhases];
+    int n1, n2;
+    Mat ma, mb, ma2, mb2;
+    int M, N, K, K2;
+    int goff;            // rows between the two groups (0: two matrices of the same rows)
+    int tm, tn, splits;  // tiles along M and N, pieces of K
+    int kper;            // terms of a piece (a multiple of kBK)
+    // outputs
+    void *o0, *o1, *o2;  // stored rows; planes: first plane of each
+    long long ldo, osb;  // row stride, batch stride of the output
+    int oL;              // positions of a batch entry of the output
+    long long plane;     // distance of the planes of an output
+    int npl;             // planes written (1 or 3)
+    int act;
+    bool out32;          // fp32 output (else bf16)
+};
+
+enum { kEpiOut = 0, kEpiGate = 1, kEpiGrad = 2, kEpiPart = 3 };
+
+template <int WM_, int WN_, int MT_, int NT_>
+struct TileCfg {
+    static constexpr int WM = WM_, WN = WN_, MT = MT_, NT = NT_;
+    static constexpr int NTH = 64 * WM * WN;
+    static constexpr int BMG = 32 * WM * MT;  // rows of a group
+    static constexpr int BN = 32 * WN * NT;
+    static constexpr int kAB = 2 * BMG * kBK * 2, kBB = BN * kBK * 2;  // bytes of a stage
+    static constexpr int NA = 2 * BMG * 8 / NTH, NB = BN * 8 / NTH;    // 16-byte pieces a thread loads per stage
+};
+
+typedef __attribute__((address_space(3))) void lds_void;
+
+// 16 bytes a lane from global memory to LDS at the wave-uniform address l plus
+// 16 times the lane.  In assembly because the compiler, which cannot tell the
+// stage being filled from the one being read, waits for the builtin's load
+// before the next LDS read.  The instruction has no destination register; it is
+// complete at wait_loads(), which comes before the barrier ahead of its use.
+__device__ __forceinline__ void to_lds(const void* g, unsigned l)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(l), "v"(g) : "memory");
+}
+
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+__device__ __forceinline__ unsigned lds_address(const void* p)
+{
+    return (unsigned)(unsigned long long)(lds_void*)p;
+}
+
+// The product of one stage: fragments of 16 terms from LDS, four steps.  aoff
+// and boff are the lane's read offsets, swa its piece swizzle.
+template <class Cfg, int G, bool BTR>
+__device__ __forceinline__ void stage_product(const char* sa, const char* sb, int aoff,
+                                              const int (&boff)[Cfg::NT], int h, int swa,
+                                              f32x16 (&acc)[G][Cfg::MT][Cfg::NT])
+{
+    constexpr int BN = Cfg::BN, BMG = Cfg::BMG;
+#pragma unroll
+    for (int ks = 0; ks < kBK / 16; ++ks) {
+        bf16x8 fa[G][Cfg::MT], fb[Cfg::NT];
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int i = 0; i < Cfg::MT; ++i)
+                fa[g][i] = *reinterpret_cast<const bf16x8*>(sa + g * (BMG * 128) + aoff + i * (32 * 128) +
+                                                             (((ks * 2 + h) ^ swa) << 4));
+#pragma unroll
+        for (int j = 0; j < Cfg::NT; ++j) {
+            if constexpr (BTR) {
+                typedef __attribute__((address_space(3))) s16x4 lds4;
+                const char* q = sb + boff[j] + ks * (16 * BN * 2);
+                const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)q);
+                const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(q + 4 * BN * 2));
+                fb[j] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+            } else {
+                fb[j] = *reinterpret_cast<const bf16x8*>(sb + boff[j] + (((ks * 2 + h) ^ swa) << 4));
+            }
+        }
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int i = 0; i < Cfg::MT; ++i)
+#pragma unroll
+                for (int j = 0; j < Cfg::NT; ++j)
+                    // Columns of B along the accumulator's rows: a lane then holds runs of
+                    // four consecutive columns of one row of the result.
+                    acc[g][i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[j], fa[g][i], acc[g][i][j], 0, 0, 0);
+    }
+}
+
+// Sum over phases [p0, p0 + np) into acc, G row groups.
+template <class Cfg, int G, bool BTR>
+__device__ __forceinline__ void tile_product(const TileArgs& a, int p0, int np, const Mat& ma, const Mat& mb, int K,
+                                             int kb, int ke, int m0, int n0, char* As, char* Bs,
+                                             f32x16 (&acc)[G][Cfg::MT][Cfg::NT])
+{
+    constexpr int NTH = Cfg::NTH, BN = Cfg::BN, BMG = Cfg::BMG;
+    constexpr int NA = G * BMG * 8 / NTH, NB = Cfg::NB;
+    const int t = (int)threadIdx.x, lane = t & 63;
+    const int w = __builtin_amdgcn_readfirstlane(t >> 6), wm = w / Cfg::WN, wn = w % Cfg::WN;
+    const int steps = (ke - kb + kBK - 1) / kBK;
+    if (steps <= 0 || np <= 0) return;
+    // This thread's pieces.  k-contiguous tiles are [row][8 pieces of 8 terms],
+    // piece c of row r in slot c ^ (r / 2 % 8): 16 rows of one piece then cover
+    // all 64 banks.  Column-contiguous tiles are [term][BN / 8 pieces], piece c
+    // of term k in slot c ^ (k % 4 * 4): the four terms of a transposing read
+    // then lie in different 64-byte quarters of the banks.
+    const int ar = t >> 3, ac = ((t & 7) ^ ((t >> 4) & 7)) * 8;
+    const __bf16 *pa[NA], *pb[NB];
+    int la = 0, lb = 0;
+    const auto rows = [&](const __bf16* base, const Mat& m, int row, long long koff) {
+        return base + (long long)row * m.ld + koff;
+    };
+    const auto start = [&](int p) {
+        const long long k = kb + ac, qa = ma.L > k ? 0 : k / ma.L;
+        la = (int)(k - qa * ma.L);
+#pragma unroll
+        for (int j = 0; j < NA; ++j) {
+            const int r = j * (NTH / 8) + ar, g = G > 1 && r >= BMG ? 1 : 0;
+            int row = m0 + (r - g * BMG) + (g ? a.goff : 0);
+            row = row < a.M ? row : a.M - 1;  // rows past the end are computed and not stored
+            pa[j] = rows(g ? a.A1[p] : a.A0[p], ma, row, qa * ma.sb + la);
+        }
+        if constexpr (BTR) {
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                const int e = j * NTH + t, kk = e / (BN / 8), c = (e % (BN / 8)) ^ ((kk & 3) << 2);
+                int n = n0 + c * 8;
+                n = n < a.N ? n : 0;
+                const int q = n / mb.L;
+                pb[j] = a.B[p] + (long long)(kb + kk) * mb.ld + q * mb.sb + (n - q * mb.L);
+            }
+        } else {
+            const long long q = mb.L > k ? 0 : k / mb.L;
+            lb = (int)(k - q * mb.L);
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                int row = n0 + j * (NTH / 8) + ar;
+                row = row < a.N ? row : a.N - 1;
+                pb[j] = rows(a.B[p], mb, row, q * mb.sb + lb);
+            }
+        }
+    };
+    int ip = p0, ik = kb;
+    const unsigned lds0 = lds_address(As) + w * 1024, ldsb = lds_address(Bs) + w * 1024;
+    const auto issue = [&](int buf) {
+        const void* z = g_zeros;
+        const unsigned da = lds0 + buf * Cfg::kAB, db = ldsb + buf * Cfg::kBB;
+        const bool oka = ik + ac < K;
+#pragma unroll
+        for (int j = 0; j < NA; ++j) {
+            to_lds(oka ? (const void*)pa[j] : z, da + j * (NTH * 16));
+            pa[j] += kBK;
+        }
+        la += kBK;
+        while (la >= ma.L) {
+            la -= ma.L;
+#pragma unroll
+            for (int j = 0; j < NA; ++j) pa[j] += ma.sb - ma.L;
+        }
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+            const bool ok = BTR ? ik + (j * NTH + t) / (BN / 8) < K : oka;
+            to_lds(ok ? (const void*)pb[j] : z, db + j * (NTH * 16));
+            pb[j] += BTR ? (long long)kBK * mb.ld : (long long)kBK;
+        }
+        if constexpr (!BTR) {
+            lb += kBK;
+            while (lb >= mb.L) {
+                lb -= mb.L;
+#pragma unroll
+                for (int j = 0; j < NB; ++j) pb[j] += mb.sb - mb.L;
+            }
+        }
+        ik += kBK;
+        if (ik >= ke) {
+            ik = kb;
+            if (++ip < p0 + np) start(ip);
+        }
+    };
+    // Read addresses.
+    const int h = lane >> 5, swa = (lane >> 1) & 7;
+    const int arow = (wm * Cfg::MT * 32 + (lane & 31)) * 128;
+    int boff[Cfg::NT];
+#pragma unroll
+    for (int j = 0; j < Cfg::NT; ++j) {
+        const int nb = (wn * Cfg::NT + j) * 32;
+        if constexpr (BTR) {
+            const int i = lane & 15, kk = 8 * h + (i >> 2);
+            boff[j] = kk * (BN * 2) + (((nb >> 5) ^ (i >> 2)) << 6) + ((lane >> 4) & 1) * 32 + (i & 3) * 8;
+        } else {
+            boff[j] = (nb + (lane & 31)) * 128;
+        }
+    }
+    start(p0);
+    issue(0);
+    const int total = steps * np;
+    for (int it = 0; it < total; ++it) {
+        wait_loads();
+        __syncthreads();  // this stage has arrived; the other one is no longer read
+        if (it + 1 < total) issue((it + 1) & 1);
+        stage_product<Cfg, G, BTR>(As + (it & 1) * Cfg::kAB, Bs + (it & 1) * Cfg::kBB, arow, boff, h, swa, acc);
+    }
+}
+
+__device__ __forceinline__ float truncated(float v)
+{
+    return __builtin_bit_cast(float, __builtin_bit_cast(unsigned, v) & 0xffff0000u);
+}
+
+// The three planes of v (see above).  Non-finite values keep their leading
+// plane alone.
+__device__ __forceinline__ void split3(float v, float (&p)[3])
+{
+    p[0] = truncated(v);
+    // A NaN whose payload lies in the low half would lose it.
+    if (v != v) p[0] = v;
+    const bool fin = __builtin_fabsf(p[0]) < __builtin_inff();
+    const float r = fin ? v - p[0] : 0.0f;
+    p[1] = truncated(r);
+    p[2] = r - p[1];
+}
+
+// Four consecutive columns n.. of row m into the planes of an intermediate
+// matrix (row stride ldo); columns past N are written as zeros up to the row's
+// padding, where the weight gradients read them as terms.
+__device__ __forceinline__ void store_plane(const TileArgs& a, void* o, int m, int n, float (&f)[4])
+{
+    if (n >= a.ldo) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (n + i >= a.N) f[i] = 0.0f;
+    __bf16* q = (__bf16*)o + (long long)m * a.ldo + n;
+    if (a.npl == 1) {
+        store_pack<__bf16, 4>(q, f, 4);
+    } else {
+        float s[3][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float p[3];
+            split3(f[i], p);
+#pragma unroll
+            for (int k = 0; k < 3; ++k) s[k][i] = p[k];
+        }
+#pragma unroll
+        for (int k = 0; k < 3; ++k) store_pack<__bf16, 4>(q + k * a.plane, s[k], 4);
+    }
+}
+
+// Four consecutive columns into a result of the caller's layout.
+template <class T>
+__device__ __forceinline__ void store_out(const TileArgs& a, void* o, int m, int n, const float (&f)[4])
+{
+    if (n >= a.N) return;
+    T* r = (T*)o + (long long)m * a.ldo;
+    const int q = n / a.oL, l = n - q * a.oL;
+    if (n + 4 <= a.N && l + 4 <= a.oL) {
+        store_pack<T, 4>(r + q * a.osb + l, f, 4);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int c = n + i;
+        if (c >= a.N) break;
+        const int qq = c / a.oL;
+        r[qq * a.osb + (c - qq * a.oL)] = (T)f[i];
+    }
+}
+
+template <class Cfg, bool BTR, int EPI>
+__global__ __launch_bounds__(Cfg::NTH) void k_ffn_tile(TileArgs a)
+{
+    __shared__ __align__(1024) char As[2 * Cfg::kAB];
+    __shared__ __align__(1024) char Bs[2 * Cfg::kBB];
+    const int tiles = a.tm * a.tn;
+    const int id = (int)blockIdx.x, s = id / tiles, tile = id - s * tiles;
+    const int m0 = (tile % a.tm) * (a.goff ? 2 * Cfg::BMG : Cfg::BMG), n0 = (tile / a.tm) * Cfg::BN;
+    const int kb = s * a.kper, ke = kb + a.kper < a.K ? kb + a.kper : a.K;
+    f32x16 acc[2][Cfg::MT][Cfg::NT] = {};
+    tile_product<Cfg, 2, BTR>(a, 0, a.n1, a.ma, a.mb, a.K, kb, ke, m0, n0, As, Bs, acc);
+    f32x16 dh[1][Cfg::MT][Cfg::NT] = {};
+    if constexpr (EPI == kEpiGrad) {
+        __syncthreads();
+        tile_product<Cfg, 1, BTR>(a, a.n1, a.n2, a.ma2, a.mb2, a.K2, 0, a.K2, m0, n0, As, Bs, dh);
+    }
+    const int t = (int)threadIdx.x, lane = t & 63, w = t >> 6, wm = w / Cfg::WN, wn = w % Cfg::WN;
+#pragma unroll
+    for (int i = 0; i < Cfg::MT; ++i)
+#pragma unroll
+        for (int j = 0; j < Cfg::NT; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int m = m0 + (wm * Cfg::MT + i) * 32 + (lane & 31);
+                const int n = n0 + (wn * Cfg::NT + j) * 32 + 8 * q + 4 * (lane >> 5);
+                float f[2][4];
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) f[g][r] = acc[g][i][j][4 * q + r];
+                if constexpr (EPI == kEpiOut || EPI == kEpiPart) {
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        const int mg = m + g * a.goff;
+                        if (mg >= a.M) continue;
+                        void* o = g && !a.goff ? a.o1 : a.o0;
+                        if constexpr (EPI == kEpiPart) {
+                            if (a.splits > 1) {
+                                // [piece][row][column], the second matrix's rows behind the first's
+                                float* d = (float*)a.o2 + ((long long)s * (a.goff ? a.M : 2 * a.M) + mg +
+                                                           (g && !a.goff ? a.M : 0)) * a.N + n;
+#pragma unroll
+                                for (int r = 0; r < 4; ++r)
+                                    if (n + r < a.N) d[r] = f[g][r];
+                                continue;
+                            }
+                        }
+                        if (a.out32) store_out<float>(a, o, mg, n, f[g]);
+                        else store_out<__bf16>(a, o, mg, n, f[g]);
+                    }
+                } else if constexpr (EPI == kEpiGate) {
+                    if (m >= a.M) continue;
+                    float hv[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) hv[r] = act_fwd(a.act, f[0][r]) * f[1][r];
+                    store_plane(a, a.o0, m, n, hv);
+                } else {
+                    if (m >= a.M) continue;
+                    float hv[4], dg[4], du[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        float ga, da;
+                        act_both(a.act, f[0][r], ga, da);
+                        const float d = dh[0][i][j][4 * q + r];
+                        hv[r] = ga * f[1][r];
+                        dg[r] = d * f[1][r] * da;
+                        du[r] = d * ga;
+                    }
+                    store_plane(a, a.o0, m, n, hv);
+                    store_plane(a, a.o1, m, n, dg);
+                    store_plane(a, a.o2, m, n, du);
+                }
+            }
+}
+
+}  // namespace
+}  // namespace hyenand

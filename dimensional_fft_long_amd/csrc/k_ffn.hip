@@ -1,197 +1,85 @@
-// k_ffn.hip -- the gated feed-forward block, forward and backward: products of
-// weights and activations with the activation and the gate product in their
-// epilogues.
-#include "block_dev.h"
+// k_ffn.hip -- the gated feed-forward block, forward and backward: the launch
+// chains over the matrix-core product of ffn_tile.h, operands brought into its
+// layout, and the weight gradients' sum over pieces.
+//
+//   forward   h  = a(Wg x) (Wu x)            one launch, both products and the gate in its epilogue
+//             y  = Wd h
+//   backward  g, u, dh = Wd^T dy -> h, dg, du  one launch: g, u and dh stay in the accumulators
+//             dx = Wg^T dg + Wu^T du          one launch, both products into one accumulator
+//             dWg, dWu = dg x^T, du x^T       one launch (x is read once for both)
+//             dWd = dy h^T
+//
+// The hidden values are planes [F][positions of all batch entries], padded to
+// eight.  Operands are used where they lie if their rows are multiples of 16
+// bytes (bf16, C, F and L multiples of eight); else, and for fp32, a pass
+// writes them as padded bf16 planes first.
+#include "ffn_tile.h"
+
+#include <climits>
 
 namespace hyenand {
 namespace {
 
-// A matrix of activations or weights: element (r, t) at
-// r * sr + (t / L) * sb + (t % L) * st.
+constexpr long long kFar = 1ll << 62;
+
+// Source of a pass: element (r, t) at r * sr + (t / L) * sb + (t % L) * st.
 struct View {
     const void* p;
     long long sr, st, L, sb;
 };
 
-struct GemmArgs {
-    View A[2], B[2];  // C[n] = sum_k A[n](m, k) B[n](k, t): k is B's row index, or its column index with BT
-    int nprod;        // products (accumulated into one result, or kept apart with DUAL)
-    int M, N;
-    long long K;
-    void *o0, *o1, *o2;            // outputs, [M][ldo] or through oL / osb
-    const void *i0, *i1;           // saved g and u (backward epilogue)
-    long long osr, oL, osb;
-    int act;
-};
-
-template <class T>
-__device__ __forceinline__ float at(const View& v, long long r, long long t)
+template <class T, int NPL>
+__global__ __launch_bounds__(256) void k_ffn_pack(View v, int rows, int cols, int ld, __bf16* dst, long long plane,
+                                                  bool by_row)
 {
-    return (float)((const T*)v.p)[r * v.sr + (t / v.L) * v.sb + (t % v.L) * v.st];
-}
-
-enum { kEpiStore = 0, kEpiGate = 1, kEpiGrad = 2 };
-
-// 64 x 64 outputs by 256 threads, 4 x 4 each, through LDS tiles of 16 terms.
-template <class T, bool BT, int EPI>
-__global__ __launch_bounds__(256) void k_ffn_gemm(GemmArgs a)
-{
-    __shared__ float As[16][65], Bs[16][65];
-    constexpr int NACC = EPI == kEpiGate ? 2 : 1;
-    const int t = (int)threadIdx.x, tx = t & 15, ty = t >> 4;
-    const long long m0 = (long long)blockIdx.y * 64, n0 = (long long)blockIdx.x * 64;
-    float acc[NACC][4][4] = {};
-    for (int p = 0; p < a.nprod; ++p) {
-        const View va = a.A[p], vb = a.B[p];
-        for (long long k0 = 0; k0 < a.K; k0 += 16) {
-            for (int i = t; i < 1024; i += 256) {
-                const int kk = i >> 6, c = i & 63;
-                const long long k = k0 + kk;
-                As[kk][c] = (k < a.K && m0 + c < a.M) ? at<T>(va, m0 + c, k) : 0.0f;
-                Bs[kk][c] = (k < a.K && n0 + c < a.N) ? (BT ? at<T>(vb, n0 + c, k) : at<T>(vb, k, n0 + c)) : 0.0f;
-            }
-            __syncthreads();
-            for (int kk = 0; kk < 16; ++kk) {
-                float ra[4], rb[4];
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    const int gc = ld / 8;
+    // Threads along the direction that is contiguous in the source.
+    const long long r = by_row ? i % rows : i / gc, g = by_row ? i / rows : i % gc;
+    if (r >= rows || g >= gc) return;
+    const long long t0 = g * 8;
+    float f[8];
+    const long long q = t0 / v.L, l = t0 - q * v.L;
+    const T* s = (const T*)v.p + r * v.sr;
+    if (v.st == 1 && t0 + 8 <= cols && l + 8 <= v.L) {
+        const Pack<T, 8> k = load_pack<T, 8>(s + q * v.sb + l, 8);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    ra[i] = As[kk][ty * 4 + i];
-                    rb[i] = Bs[kk][tx * 4 + i];
-                }
+        for (int j = 0; j < 8; ++j) f[j] = k.get(j);
+    } else {
 #pragma unroll
-                for (int n = 0; n < NACC; ++n)
-                    if (NACC == 1 || n == p)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) acc[n][i][j] += ra[i] * rb[j];
-            }
-            __syncthreads();
+        for (int j = 0; j < 8; ++j) {
+            const long long t = t0 + j, qq = t / v.L;
+            f[j] = t < cols ? (float)s[qq * v.sb + (t - qq * v.L) * v.st] : 0.0f;
         }
     }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const long long m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-            if (m >= a.M || n >= a.N) continue;
-            const long long o = m * a.osr + (n / a.oL) * a.osb + n % a.oL;
-            if constexpr (EPI == kEpiStore) {
-                ((T*)a.o0)[o] = (T)acc[0][i][j];
-            } else if constexpr (EPI == kEpiGate) {
-                const float g = acc[0][i][j], u = acc[NACC - 1][i][j];
-                ((T*)a.o0)[o] = (T)(act_fwd(a.act, g) * u);
-                if (a.o1) {
-                    ((T*)a.o1)[o] = (T)g;
-                    ((T*)a.o2)[o] = (T)u;
-                }
-            } else {
-                const float g = (float)((const T*)a.i0)[o], u = (float)((const T*)a.i1)[o], dh = acc[0][i][j];
-                float ga, da;
-                act_both(a.act, g, ga, da);
-                ((T*)a.o1)[o] = (T)(dh * u * da);
-                ((T*)a.o2)[o] = (T)(dh * ga);
-            }
+    __bf16* d = dst + r * ld + t0;
+    if constexpr (NPL == 1) {
+        store_pack<__bf16, 8>(d, f, 8);
+    } else {
+        float s3[3][8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float p[3];
+            split3(f[j], p);
+#pragma unroll
+            for (int k = 0; k < 3; ++k) s3[k][j] = p[k];
         }
-}
-
-template <class T, bool BT, int EPI>
-hipError_t gemm(const GemmArgs& a, hipStream_t st)
-{
-    if (a.M <= 0 || a.N <= 0) return hipSuccess;
-    hipLaunchKernelGGL((k_ffn_gemm<T, BT, EPI>), dim3((unsigned)((a.N + 63) / 64), (unsigned)((a.M + 63) / 64)),
-                       dim3(256), 0, st, a);
-    return launch_status();
-}
-
-constexpr long long kFar = 1ll << 62;
-
-template <class T>
-hipError_t forward(const FfnArgs& a, bool save, hipStream_t st)
-{
-    const long long Tn = a.B * a.L;
-    T* h = (T*)a.ws;
-    const View x{a.x, a.L, 1, a.L, a.C * a.L}, wg{a.Wg, a.C, 1, kFar, 0}, wu{a.Wu, a.C, 1, kFar, 0};
-    GemmArgs g{};
-    g.A[0] = wg;
-    g.A[1] = wu;
-    g.B[0] = g.B[1] = x;
-    g.nprod = 2;
-    g.M = a.F;
-    g.N = (int)Tn;
-    g.K = a.C;
-    g.o0 = h;
-    if (save) {
-        g.o1 = h + a.F * Tn;
-        g.o2 = h + 2 * a.F * Tn;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) store_pack<__bf16, 8>(d + k * plane, s3[k], 8);
     }
-    g.osr = Tn;
-    g.oL = kFar;
-    g.act = a.act;
-    hipError_t e = gemm<T, false, kEpiGate>(g, st);
-    if (e != hipSuccess || save) return e;
-    GemmArgs d{};
-    d.A[0] = View{a.Wd, a.F, 1, kFar, 0};
-    d.B[0] = View{h, Tn, 1, kFar, 0};
-    d.nprod = 1;
-    d.M = a.C;
-    d.N = (int)Tn;
-    d.K = a.F;
-    d.o0 = a.y;
-    d.osr = a.L;
-    d.oL = a.L;
-    d.osb = a.C * a.L;
-    return gemm<T, false, kEpiStore>(d, st);
 }
 
+// Weight gradients: the pieces' partial sums [splits][rows][N] in order, the
+// first M rows to o0 and the rest to o1.
 template <class T>
-hipError_t backward(const FfnArgs& a, hipStream_t st)
+__global__ __launch_bounds__(256) void k_ffn_sum(const float* part, int splits, long long n, long long n0, T* o0, T* o1)
 {
-    const long long Tn = a.B * a.L;
-    T *h = (T*)a.ws, *dg = h + a.F * Tn, *du = dg + a.F * Tn;
-    const View x{a.x, a.L, 1, a.L, a.C * a.L}, dy{a.dy, a.L, 1, a.L, a.C * a.L};
-    const View vh{h, Tn, 1, kFar, 0}, vdg{dg, Tn, 1, kFar, 0}, vdu{du, Tn, 1, kFar, 0};
-    hipError_t e = forward<T>(a, true, st);  // h, g, u
-    if (e != hipSuccess) return e;
-    GemmArgs g{};
-    g.A[0] = View{a.Wd, 1, a.F, kFar, 0};  // Wd^T
-    g.B[0] = dy;
-    g.nprod = 1;
-    g.M = a.F;
-    g.N = (int)Tn;
-    g.K = a.C;
-    g.i0 = g.o1 = dg;  // g and u are read and replaced by their gradients
-    g.i1 = g.o2 = du;
-    g.osr = Tn;
-    g.oL = kFar;
-    g.act = a.act;
-    if ((e = gemm<T, false, kEpiGrad>(g, st)) != hipSuccess) return e;
-    GemmArgs d{};
-    d.A[0] = View{a.Wg, 1, a.C, kFar, 0};
-    d.A[1] = View{a.Wu, 1, a.C, kFar, 0};
-    d.B[0] = vdg;
-    d.B[1] = vdu;
-    d.nprod = 2;
-    d.M = a.C;
-    d.N = (int)Tn;
-    d.K = a.F;
-    d.o0 = a.dx;
-    d.osr = a.L;
-    d.oL = a.L;
-    d.osb = a.C * a.L;
-    if ((e = gemm<T, false, kEpiStore>(d, st)) != hipSuccess) return e;
-    for (int i = 0; i < 3; ++i) {
-        GemmArgs w{};
-        w.A[0] = i == 0 ? vdg : i == 1 ? vdu : dy;
-        w.B[0] = i < 2 ? x : vh;
-        w.nprod = 1;
-        w.M = i < 2 ? a.F : a.C;
-        w.N = i < 2 ? a.C : a.F;
-        w.K = Tn;
-        w.o0 = i == 0 ? a.dWg : i == 1 ? a.dWu : a.dWd;
-        w.osr = w.N;
-        w.oL = kFar;
-        if ((e = gemm<T, true, kEpiStore>(w, st)) != hipSuccess) return e;
-    }
-    return hipSuccess;
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n) return;
+    float s = 0.0f;
+    for (int p = 0; p < splits; ++p) s += part[(long long)p * n + i];
+    if (i < n0) o0[i] = (T)s;
+    else o1[i - n0] = (T)s;
 }
 
 __global__ __launch_bounds__(256) void k_ffn_zero(unsigned short* p, long long n)
@@ -199,6 +87,316 @@ __global__ __launch_bounds__(256) void k_ffn_zero(unsigned short* p, long long n
     const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
     if (i < n) p[i] = 0;
 }
+
+typedef TileCfg<2, 4, 2, 2> Big;  // 128 (x 2 groups) x 256, 512 threads, one workgroup per CU
+typedef TileCfg<2, 2, 1, 2> Mid;  // 64 (x 2 groups) x 128, 256 threads, two workgroups per CU
+constexpr int kCUs = 256;
+
+long long round8(long long v) { return (v + 7) & ~7ll; }
+
+// A packed operand or intermediate: planes of [rows][ld].
+struct Planes {
+    __bf16* p;
+    long long ld, plane;
+};
+
+// How the weight gradients' sum over positions is cut: pieces of whole stages so
+// that the tiles fill the device's workgroup slots, weighed against the partial
+// sums' traffic (time in units of one stage of the big tile, about a microsecond).
+int pieces(long long tiles, int slots, long long K, long long elems)
+{
+    const long long steps = (K + kBK - 1) / kBK;
+    double best = 0.0;
+    int pick = 1;
+    for (int s = 1; s <= 128 && s <= steps; ++s) {
+        const double waves = (double)((tiles * s + slots - 1) / slots), per = (double)((steps + s - 1) / s);
+        const double cost = waves * (per + 6.0) + (s > 1 ? 10.0 + (double)elems * s * 8.0 / 4.0e6 : 0.0);
+        if (s == 1 || cost < best) best = cost, pick = s;
+    }
+    return pick;
+}
+
+bool use_big(long long rows, long long cols, int groups_rows)
+{
+    return ((rows + groups_rows - 1) / groups_rows) * ((cols + Big::BN - 1) / Big::BN) >= kCUs * 3 / 4;
+}
+
+struct Cut {
+    bool big;
+    int splits;
+};
+
+Cut cut_dw(long long rows, long long cols, long long K, bool dual)
+{
+    const long long t_big = ((rows + (dual ? 1 : 2) * Big::BMG - 1) / ((dual ? 1 : 2) * Big::BMG)) *
+                            ((cols + Big::BN - 1) / Big::BN);
+    const long long t_mid = ((rows + (dual ? 1 : 2) * Mid::BMG - 1) / ((dual ? 1 : 2) * Mid::BMG)) *
+                            ((cols + Mid::BN - 1) / Mid::BN);
+    const long long elems = rows * cols * (dual ? 2 : 1);
+    const bool big = rows >= Big::BMG && cols >= Big::BN;
+    return Cut{big, big ? pieces(t_big, kCUs, K, elems) : pieces(t_mid, 2 * kCUs, K, elems)};
+}
+
+struct Layout {
+    int npl;
+    long long T, Tp, Cp, Fp;
+    bool xdirect, wdirect;
+    size_t h, dg, du, x, dy, wg, wu, wd, wgt, wut, wdt, part, total;
+};
+
+Layout layout(int B, int C, int F, long long L, bool bf16, bool bwd)
+{
+    Layout o{};
+    o.npl = bf16 ? 1 : 3;
+    o.T = B * L;
+    o.Tp = round8(o.T);
+    o.Cp = round8(C);
+    o.Fp = round8(F);
+    o.xdirect = bf16 && L % 8 == 0;
+    o.wdirect = bf16 && C % 8 == 0 && F % 8 == 0;
+    size_t at = 0;
+    const auto take = [&](size_t& off, long long rows, long long ld) {
+        off = at;
+        at += ((size_t)rows * (size_t)ld * 2u * (size_t)o.npl + 255u) & ~(size_t)255u;
+    };
+    take(o.h, F, o.Tp);
+    if (!o.xdirect) take(o.x, C, o.Tp);
+    if (!o.wdirect) {
+        take(o.wg, F, o.Cp);
+        take(o.wu, F, o.Cp);
+        if (!bwd) take(o.wd, C, o.Fp);
+    }
+    if (bwd) {
+        take(o.dg, F, o.Tp);
+        take(o.du, F, o.Tp);
+        if (!o.xdirect) take(o.dy, C, o.Tp);
+        take(o.wgt, C, o.Fp);
+        take(o.wut, C, o.Fp);
+        take(o.wdt, F, o.Cp);
+        const Cut c1 = cut_dw(F, C, o.T, true), c2 = cut_dw(C, F, o.T, false);
+        const size_t e1 = c1.splits > 1 ? (size_t)c1.splits * 2u : 0u, e2 = c2.splits > 1 ? (size_t)c2.splits : 0u;
+        o.part = at;
+        at += (e1 > e2 ? e1 : e2) * (size_t)F * (size_t)C * 4u;
+    }
+    o.total = at;
+    return o;
+}
+
+template <class Cfg, bool BTR, int EPI>
+hipError_t run_tiles(TileArgs& a, hipStream_t st)
+{
+    const long long gm = a.goff ? 2 * Cfg::BMG : Cfg::BMG;
+    if (a.goff) a.goff = Cfg::BMG;
+    const long long tm = (a.M + gm - 1) / gm, tn = ((long long)a.N + Cfg::BN - 1) / Cfg::BN;
+    if (tm * tn * a.splits > INT_MAX) return hipErrorInvalidValue;
+    a.tm = (int)tm;
+    a.tn = (int)tn;
+    hipLaunchKernelGGL((k_ffn_tile<Cfg, BTR, EPI>), dim3((unsigned)(tm * tn * a.splits)), dim3(Cfg::NTH), 0, st, a);
+    return launch_status();
+}
+
+template <bool BTR, int EPI>
+hipError_t run_any(TileArgs& a, bool big, hipStream_t st)
+{
+    return big ? run_tiles<Big, BTR, EPI>(a, st) : run_tiles<Mid, BTR, EPI>(a, st);
+}
+
+// The phases of one product: pairs of planes, smallest first.
+int add_phases(TileArgs& a, int at, int npl, const __bf16* A0, const __bf16* A1, long long pa, const __bf16* B,
+               long long pb)
+{
+    static const int ia[6] = {2, 1, 0, 1, 0, 0}, ib[6] = {0, 1, 2, 0, 1, 0};
+    for (int i = npl == 1 ? 5 : 0; i < 6; ++i, ++at) {
+        a.A0[at] = A0 + ia[i] * pa;
+        a.A1[at] = A1 + ia[i] * pa;
+        a.B[at] = B + ib[i] * pb;
+    }
+    return at;
+}
+
+struct Chain {
+    const FfnArgs& f;
+    Layout o;
+    hipStream_t st;
+    char* ws;
+
+    Chain(const FfnArgs& a, bool bwd, hipStream_t s)
+        : f(a), o(layout(a.B, a.C, a.F, a.L, a.bf16, bwd)), st(s), ws((char*)a.ws)
+    {
+    }
+    Planes planes(size_t off, long long rows, long long ld) const { return {(__bf16*)(ws + off), ld, rows * ld}; }
+
+    hipError_t pack(const View& v, int rows, int cols, const Planes& d, bool by_row) const
+    {
+        const long long n = rows * (d.ld / 8);
+        const unsigned grid = (unsigned)((n + 255) / 256);
+        if (f.bf16)
+            hipLaunchKernelGGL((k_ffn_pack<__bf16, 1>), dim3(grid), dim3(256), 0, st, v, rows, cols, (int)d.ld, d.p,
+                               d.plane, by_row);
+        else
+            hipLaunchKernelGGL((k_ffn_pack<float, 3>), dim3(grid), dim3(256), 0, st, v, rows, cols, (int)d.ld, d.p,
+                               d.plane, by_row);
+        return launch_status();
+    }
+
+    // Activations [B][C][L] as an operand: where they lie, or packed at off.
+    hipError_t act(const void* x, size_t off, Planes* p, Mat* m) const
+    {
+        if (o.xdirect) {
+            *p = Planes{(__bf16*)x, f.L, 0};
+            *m = Mat{f.L, f.C * f.L, (int)f.L};
+            return hipSuccess;
+        }
+        *p = planes(off, f.C, o.Tp);
+        *m = Mat{o.Tp, 0, INT_MAX};
+        // One position per batch entry: rows of channels, read along them.
+        const View v = f.L == 1 ? View{x, 1, f.C, kFar, 0} : View{x, f.L, 1, f.L, f.C * f.L};
+        return pack(v, f.C, (int)o.T, *p, f.L == 1);
+    }
+
+    hipError_t weight(const void* w, size_t off, int rows, int cols, Planes* p, Mat* m) const
+    {
+        const long long ld = o.wdirect ? cols : round8(cols);
+        *m = Mat{ld, 0, INT_MAX};
+        if (o.wdirect) {
+            *p = Planes{(__bf16*)w, ld, 0};
+            return hipSuccess;
+        }
+        *p = planes(off, rows, ld);
+        return pack(View{w, cols, 1, kFar, 0}, rows, cols, *p, false);
+    }
+
+    // w [cols][rows] transposed.
+    hipError_t weight_t(const void* w, size_t off, int rows, int cols, Planes* p, Mat* m) const
+    {
+        const long long ld = round8(cols);
+        *m = Mat{ld, 0, INT_MAX};
+        *p = planes(off, rows, ld);
+        return pack(View{w, 1, rows, kFar, 0}, rows, cols, *p, true);
+    }
+
+    TileArgs base(int M, long long N, int K) const
+    {
+        TileArgs a{};
+        a.M = M;
+        a.N = (int)N;
+        a.K = a.kper = K;
+        a.splits = 1;
+        a.act = f.act;
+        a.npl = o.npl;
+        a.out32 = !f.bf16;
+        a.oL = INT_MAX;
+        return a;
+    }
+
+    // y or dx: rows of C channels in the caller's layout.
+    void to_grid(TileArgs& a, void* out) const
+    {
+        a.o0 = out;
+        a.ldo = f.L;
+        a.osb = f.C * f.L;
+        a.oL = (int)f.L;
+        a.goff = 1;
+    }
+
+    hipError_t forward() const
+    {
+        Planes x, wg, wu, wd, h = planes(o.h, f.F, o.Tp);
+        Mat mx, mw, md;
+        hipError_t e;
+        if ((e = act(f.x, o.x, &x, &mx)) != hipSuccess || (e = weight(f.Wg, o.wg, f.F, f.C, &wg, &mw)) != hipSuccess ||
+            (e = weight(f.Wu, o.wu, f.F, f.C, &wu, &mw)) != hipSuccess ||
+            (e = weight(f.Wd, o.wd, f.C, f.F, &wd, &md)) != hipSuccess)
+            return e;
+        TileArgs a = base(f.F, o.T, f.C);
+        a.n1 = add_phases(a, 0, o.npl, wg.p, wu.p, wg.plane, x.p, x.plane);
+        a.ma = mw;
+        a.mb = mx;
+        a.o0 = h.p;
+        a.ldo = o.Tp;
+        a.plane = h.plane;
+        if ((e = run_any<true, kEpiGate>(a, use_big(f.F, o.T, Big::BMG), st)) != hipSuccess) return e;
+        TileArgs d = base(f.C, o.T, f.F);
+        d.n1 = add_phases(d, 0, o.npl, wd.p, wd.p, wd.plane, h.p, h.plane);
+        d.ma = md;
+        d.mb = Mat{o.Tp, 0, INT_MAX};
+        to_grid(d, f.y);
+        return run_any<true, kEpiOut>(d, use_big(f.C, o.T, 2 * Big::BMG), st);
+    }
+
+    hipError_t weight_grad(TileArgs& a, bool dual, void* o0, void* o1) const
+    {
+        const Cut c = cut_dw(a.M, a.N, o.T, dual);
+        a.splits = c.splits;
+        a.kper = (int)(((o.T + kBK - 1) / kBK + c.splits - 1) / c.splits) * kBK;
+        a.goff = dual ? 0 : 1;
+        a.o0 = o0;
+        a.o1 = o1;
+        a.o2 = ws + o.part;
+        a.ldo = a.N;
+        hipError_t e = run_any<false, kEpiPart>(a, c.big, st);
+        if (e != hipSuccess || c.splits == 1) return e;
+        const long long n0 = (long long)a.M * a.N, n = n0 * (dual ? 2 : 1);
+        const unsigned grid = (unsigned)((n + 255) / 256);
+        if (f.bf16)
+            hipLaunchKernelGGL(k_ffn_sum<__bf16>, dim3(grid), dim3(256), 0, st, (const float*)a.o2, c.splits, n, n0,
+                               (__bf16*)o0, (__bf16*)o1);
+        else
+            hipLaunchKernelGGL(k_ffn_sum<float>, dim3(grid), dim3(256), 0, st, (const float*)a.o2, c.splits, n, n0,
+                               (float*)o0, (float*)o1);
+        return launch_status();
+    }
+
+    hipError_t backward() const
+    {
+        Planes x, dy, wg, wu, wgt, wut, wdt;
+        const Planes h = planes(o.h, f.F, o.Tp), dg = planes(o.dg, f.F, o.Tp), du = planes(o.du, f.F, o.Tp);
+        Mat mx, mw, mt, mdt;
+        const Mat mh{o.Tp, 0, INT_MAX};
+        hipError_t e;
+        if ((e = act(f.x, o.x, &x, &mx)) != hipSuccess || (e = act(f.dy, o.dy, &dy, &mx)) != hipSuccess ||
+            (e = weight(f.Wg, o.wg, f.F, f.C, &wg, &mw)) != hipSuccess ||
+            (e = weight(f.Wu, o.wu, f.F, f.C, &wu, &mw)) != hipSuccess ||
+            (e = weight_t(f.Wg, o.wgt, f.C, f.F, &wgt, &mt)) != hipSuccess ||
+            (e = weight_t(f.Wu, o.wut, f.C, f.F, &wut, &mt)) != hipSuccess ||
+            (e = weight_t(f.Wd, o.wdt, f.F, f.C, &wdt, &mdt)) != hipSuccess)
+            return e;
+        // h, dg, du
+        TileArgs a = base(f.F, o.T, f.C);
+        a.n1 = add_phases(a, 0, o.npl, wg.p, wu.p, wg.plane, x.p, x.plane);
+        a.n2 = add_phases(a, a.n1, o.npl, wdt.p, wdt.p, wdt.plane, dy.p, dy.plane) - a.n1;
+        a.ma = mw;
+        a.mb = a.mb2 = mx;
+        a.ma2 = mdt;
+        a.K2 = f.C;
+        a.o0 = h.p;
+        a.o1 = dg.p;
+        a.o2 = du.p;
+        a.ldo = o.Tp;
+        a.plane = h.plane;
+        if ((e = run_any<true, kEpiGrad>(a, use_big(f.F, o.T, Big::BMG), st)) != hipSuccess) return e;
+        // dx
+        TileArgs d = base(f.C, o.T, f.F);
+        const int half = add_phases(d, 0, o.npl, wgt.p, wgt.p, wgt.plane, dg.p, dg.plane);
+        d.n1 = add_phases(d, half, o.npl, wut.p, wut.p, wut.plane, du.p, du.plane);
+        d.ma = mt;
+        d.mb = mh;
+        to_grid(d, f.dx);
+        if ((e = run_any<true, kEpiOut>(d, use_big(f.C, o.T, 2 * Big::BMG), st)) != hipSuccess) return e;
+        // dWg, dWu
+        TileArgs w = base(f.F, f.C, (int)o.T);
+        w.n1 = add_phases(w, 0, o.npl, dg.p, du.p, dg.plane, x.p, x.plane);
+        w.ma = mh;
+        w.mb = mx;
+        if ((e = weight_grad(w, true, f.dWg, f.dWu)) != hipSuccess) return e;
+        // dWd
+        TileArgs v = base(f.C, f.F, (int)o.T);
+        v.n1 = add_phases(v, 0, o.npl, dy.p, dy.p, dy.plane, h.p, h.plane);
+        v.ma = mx;
+        v.mb = mh;
+        return weight_grad(v, false, f.dWd, nullptr);
+    }
+};
 
 }  // namespace
 
@@ -209,20 +407,9 @@ hipError_t launch_ffn_zero(void* p, long long bytes, hipStream_t st)
     return launch_status();
 }
 
-size_t ffn_workspace(int B, int C, int F, long long L, bool bf16, bool bwd)
-{
-    (void)C;
-    return (size_t)B * (size_t)L * (size_t)F * (bf16 ? 2u : 4u) * (bwd ? 3u : 1u);
-}
+size_t ffn_workspace(int B, int C, int F, long long L, bool bf16, bool bwd) { return layout(B, C, F, L, bf16, bwd).total; }
 
-hipError_t launch_ffn_fwd(const FfnArgs& a, hipStream_t st)
-{
-    return a.bf16 ? forward<__bf16>(a, false, st) : forward<float>(a, false, st);
-}
-
-hipError_t launch_ffn_bwd(const FfnArgs& a, hipStream_t st)
-{
-    return a.bf16 ? backward<__bf16>(a, st) : backward<float>(a, st);
-}
+hipError_t launch_ffn_fwd(const FfnArgs& a, hipStream_t st) { return Chain(a, false, st).forward(); }
+hipError_t launch_ffn_bwd(const FfnArgs& a, hipStream_t st) { return Chain(a, true, st).backward(); }
 
 }  // namespace hyenand

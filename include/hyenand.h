@@ -524,8 +524,11 @@ int hyenand_dropout(const void* x, void* y, int64_t n, int dtype, double p, cons
  * x, y: device [B][C][dims]; Wg, Wu: device [F][C]; Wd: device [C][F], all of
  * `dtype`, row-major, 16-byte aligned.  act: HYENAND_ACT_SIGMOID, _SILU or
  * _GELU.  F >= 1; C, F <= 65536 and B prod(dims) <= 2^30 (else UNSUPPORTED).
- * Products are summed in fp32; for bf16, h (and backward g, u, and their
- * gradients) round to bf16 between the products.
+ * Products are summed in fp32; for bf16, h (and backward the gradients of
+ * g and u) round to bf16 between the products.  In fp32 each operand enters
+ * the matrix cores as the exact sum of three bf16 terms, and products of terms
+ * below 2^-23 of the operands' are left out; infinities and NaN make the results
+ * that they reach non-finite.
  * workspace: device scratch, 256-byte aligned, at least the queried size;
  * contents unspecified on entry and exit.
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, HIP.

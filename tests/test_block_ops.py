@@ -350,7 +350,7 @@ FFN = [  # B, C, F, dims
     (3, 1024, 520, (1,)), (1, 64, 256, (16, 16)), (2, 128, 512, (40, 16)), (1, 100, 333, (37, 53)),
     (2, 32, 128, (8, 8, 8)), (5, 40, 96, (24,)), (3, 264, 200, (72,)), (1, 520, 1032, (264,)), (2, 129, 257, (513,)),
     (9, 16, 48, (3, 5)), (1, 8, 16, (4096,)), (1, 256, 264, (520,)), (70, 24, 40, (1,)), (300, 136, 72, (1,)),
-    (2, 320, 640, (1000,)),
+    (2, 320, 640, (1000,)), (2, 136, 520, (5120,)), (2, 136, 520, (5119,)), (1, 1032, 264, (10240,)),
 ]
 
 
