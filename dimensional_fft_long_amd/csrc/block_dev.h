@@ -2,6 +2,8 @@
 // rows at any alignment, the gate activations and the dropout generator.
 #pragma once
 
+#include <type_traits>
+
 #include "block.h"
 
 namespace hyenand {
@@ -126,6 +128,16 @@ __device__ __forceinline__ void act_both(int act, float v, float& a, float& da)
         a = s;
         da = s * q;
     }
+}
+
+// f(the activation as a constant): loops over elements then hold no branches.
+template <class F>
+__device__ __forceinline__ void with_act(int act, F&& f)
+{
+    if (act == kActSilu) f(std::integral_constant<int, kActSilu>{});
+    else if (act == kActSigmoid) f(std::integral_constant<int, kActSigmoid>{});
+    else if (act == kActGelu) f(std::integral_constant<int, kActGelu>{});
+    else f(std::integral_constant<int, kActNone>{});
 }
 
 // Four words of the counter-based generator Philox 4x32 with 10 rounds (Salmon

@@ -30,6 +30,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kBK = 64;          // terms of a stage
 constexpr int kMaxPhases = 12;
+constexpr int kTileRows = 8;     // row tiles of a band
 
 __device__ __align__(16) const unsigned g_zeros[4] = {0, 0, 0, 0};
 
@@ -92,45 +93,49 @@ __device__ __forceinline__ unsigned lds_address(const void* p)
     return (unsigned)(unsigned long long)(lds_void*)p;
 }
 
-// The product of one stage: fragments of 16 terms from LDS, four steps.  aoff
-// and boff are the lane's read offsets, swa its piece swizzle.
+// Fragments of 16 terms: row pieces of A and columns of B.
+template <class Cfg, int G>
+struct Frags {
+    bf16x8 a[G][Cfg::MT], b[Cfg::NT];
+};
+
+// aoff and boff are the lane's read offsets, swa its piece swizzle.
 template <class Cfg, int G, bool BTR>
-__device__ __forceinline__ void stage_product(const char* sa, const char* sb, int aoff,
-                                              const int (&boff)[Cfg::NT], int h, int swa,
-                                              f32x16 (&acc)[G][Cfg::MT][Cfg::NT])
+__device__ __forceinline__ void load_frags(Frags<Cfg, G>& f, const char* sa, const char* sb, int ks, int aoff,
+                                           const int (&boff)[Cfg::NT], int h, int swa)
 {
-    constexpr int BN = Cfg::BN, BMG = Cfg::BMG;
 #pragma unroll
-    for (int ks = 0; ks < kBK / 16; ++ks) {
-        bf16x8 fa[G][Cfg::MT], fb[Cfg::NT];
-#pragma unroll
-        for (int g = 0; g < G; ++g)
-#pragma unroll
-            for (int i = 0; i < Cfg::MT; ++i)
-                fa[g][i] = *reinterpret_cast<const bf16x8*>(sa + g * (BMG * 128) + aoff + i * (32 * 128) +
-                                                             (((ks * 2 + h) ^ swa) << 4));
-#pragma unroll
-        for (int j = 0; j < Cfg::NT; ++j) {
-            if constexpr (BTR) {
-                typedef __attribute__((address_space(3))) s16x4 lds4;
-                const char* q = sb + boff[j] + ks * (16 * BN * 2);
-                const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)q);
-                const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(q + 4 * BN * 2));
-                fb[j] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-            } else {
-                fb[j] = *reinterpret_cast<const bf16x8*>(sb + boff[j] + (((ks * 2 + h) ^ swa) << 4));
-            }
+    for (int j = 0; j < Cfg::NT; ++j) {
+        if constexpr (BTR) {
+            typedef __attribute__((address_space(3))) s16x4 lds4;
+            const char* q = sb + boff[j] + ks * (16 * Cfg::BN * 2);
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)q);
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(q + 4 * Cfg::BN * 2));
+            f.b[j] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        } else {
+            f.b[j] = *reinterpret_cast<const bf16x8*>(sb + boff[j] + (((ks * 2 + h) ^ swa) << 4));
         }
-#pragma unroll
-        for (int g = 0; g < G; ++g)
-#pragma unroll
-            for (int i = 0; i < Cfg::MT; ++i)
-#pragma unroll
-                for (int j = 0; j < Cfg::NT; ++j)
-                    // Columns of B along the accumulator's rows: a lane then holds runs of
-                    // four consecutive columns of one row of the result.
-                    acc[g][i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[j], fa[g][i], acc[g][i][j], 0, 0, 0);
     }
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int i = 0; i < Cfg::MT; ++i)
+            f.a[g][i] = *reinterpret_cast<const bf16x8*>(sa + g * (Cfg::BMG * 128) + aoff + i * (Cfg::WM * 32 * 128) +
+                                                         (((ks * 2 + h) ^ swa) << 4));
+}
+
+// Columns of B along the accumulator's rows: a lane then holds runs of four
+// consecutive columns of one row of the result.
+template <class Cfg, int G>
+__device__ __forceinline__ void multiply(const Frags<Cfg, G>& f, f32x16 (&acc)[G][Cfg::MT][Cfg::NT])
+{
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int i = 0; i < Cfg::MT; ++i)
+#pragma unroll
+            for (int j = 0; j < Cfg::NT; ++j)
+                acc[g][i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.b[j], f.a[g][i], acc[g][i][j], 0, 0, 0);
 }
 
 // Sum over phases [p0, p0 + np) into acc, G row groups.
@@ -225,11 +230,11 @@ __device__ __forceinline__ void tile_product(const TileArgs& a, int p0, int np, 
     };
     // Read addresses.
     const int h = lane >> 5, swa = (lane >> 1) & 7;
-    const int arow = (wm * Cfg::MT * 32 + (lane & 31)) * 128;
+    const int arow = (wm * 32 + (lane & 31)) * 128;
     int boff[Cfg::NT];
 #pragma unroll
     for (int j = 0; j < Cfg::NT; ++j) {
-        const int nb = (wn * Cfg::NT + j) * 32;
+        const int nb = (j * Cfg::WN + wn) * 32;
         if constexpr (BTR) {
             const int i = lane & 15, kk = 8 * h + (i >> 2);
             boff[j] = kk * (BN * 2) + (((nb >> 5) ^ (i >> 2)) << 6) + ((lane >> 4) & 1) * 32 + (i & 3) * 8;
@@ -240,11 +245,31 @@ __device__ __forceinline__ void tile_product(const TileArgs& a, int p0, int np, 
     start(p0);
     issue(0);
     const int total = steps * np;
+    wait_loads();
+    __syncthreads();
+    if (total > 1) issue(1);
+    // A step's fragments are read while the step before multiplies.  The barrier
+    // that ends a stage comes before its last multiplication: by then every wave
+    // has the stage's last fragments in registers, so its buffer can be filled
+    // again, and the next stage's first fragments are read behind that work.
+    Frags<Cfg, G> f0, f1;
+    load_frags<Cfg, G, BTR>(f0, As, Bs, 0, arow, boff, h, swa);
     for (int it = 0; it < total; ++it) {
-        wait_loads();
-        __syncthreads();  // this stage has arrived; the other one is no longer read
-        if (it + 1 < total) issue((it + 1) & 1);
-        stage_product<Cfg, G, BTR>(As + (it & 1) * Cfg::kAB, Bs + (it & 1) * Cfg::kBB, arow, boff, h, swa, acc);
+        const int buf = it & 1;
+        const char *sa = As + buf * Cfg::kAB, *sb = Bs + buf * Cfg::kBB;
+        load_frags<Cfg, G, BTR>(f1, sa, sb, 1, arow, boff, h, swa);
+        multiply<Cfg, G>(f0, acc);
+        load_frags<Cfg, G, BTR>(f0, sa, sb, 2, arow, boff, h, swa);
+        multiply<Cfg, G>(f1, acc);
+        load_frags<Cfg, G, BTR>(f1, sa, sb, 3, arow, boff, h, swa);
+        multiply<Cfg, G>(f0, acc);
+        if (it + 1 < total) {
+            wait_loads();
+            __syncthreads();
+            if (it + 2 < total) issue(buf);
+            load_frags<Cfg, G, BTR>(f0, As + (buf ^ 1) * Cfg::kAB, Bs + (buf ^ 1) * Cfg::kBB, 0, arow, boff, h, swa);
+        }
+        multiply<Cfg, G>(f1, acc);
     }
 }
 
@@ -266,60 +291,117 @@ __device__ __forceinline__ void split3(float v, float (&p)[3])
     p[2] = r - p[1];
 }
 
-// Four consecutive columns n.. of row m into the planes of an intermediate
-// matrix (row stride ldo); columns past N are written as zeros up to the row's
-// padding, where the weight gradients read them as terms.
-__device__ __forceinline__ void store_plane(const TileArgs& a, void* o, int m, int n, float (&f)[4])
+// Epilogue.  The accumulators' 32 x 32 blocks (i, j) of all waves form an
+// SR x SC sub-tile of consecutive rows and columns; one sub-tile at a time goes
+// through LDS (fp32, of every accumulator group) and is finished in pieces of
+// eight columns a thread: results leave in rows of 16 bytes a lane, and the
+// activation's code exists once per sub-tile instead of once per register.
+template <class Cfg>
+struct Sub {
+    static constexpr int SR = 32 * Cfg::WM, SC = 32 * Cfg::WN;
+    // Rows are 16 bytes longer than their columns: 16 rows at one column start in different banks.
+    static constexpr int LD = SC * 4 + 16, kBytes = SR * LD;
+
+    static __device__ __forceinline__ void put(char* S, const f32x16& v)
+    {
+        const int t = (int)threadIdx.x, lane = t & 63, w = t >> 6, wm = w / Cfg::WN, wn = w % Cfg::WN;
+        // A lane holds runs of four consecutive columns of one row.
+        char* d = S + (wm * 32 + (lane & 31)) * LD + (wn * 32 + 4 * (lane >> 5)) * 4;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            u32x4 o;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) o[r] = bits_of((float)v[4 * q + r]);
+            *reinterpret_cast<u32x4*>(d + q * 32) = o;
+        }
+    }
+
+    static __device__ __forceinline__ void get(const char* S, int row, int col, float (&f)[8])
+    {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const u32x4 q = *reinterpret_cast<const u32x4*>(S + row * LD + (col + 4 * k) * 4);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) f[4 * k + r] = __builtin_bit_cast(float, (unsigned)q[r]);
+        }
+    }
+
+    // piece(row, column) for every eight columns of the sub-tile.
+    template <class F>
+    static __device__ __forceinline__ void pieces(F&& piece)
+    {
+        static_assert(SR * SC / 8 % Cfg::NTH == 0);
+#pragma unroll 1
+        for (int e = (int)threadIdx.x; e < SR * SC / 8; e += Cfg::NTH) piece(e / (SC / 8), e % (SC / 8) * 8);
+    }
+};
+
+// Eight columns of row m into the planes of an intermediate matrix; columns past
+// N are written as zeros up to the row's padding, where the weight gradients
+// read them as terms.
+__device__ __forceinline__ void store_plane(const TileArgs& a, void* o, int m, int n, float (&f)[8])
 {
     if (n >= a.ldo) return;
+    if (n + 8 > a.N) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (n + i >= a.N) f[i] = 0.0f;
+        for (int i = 0; i < 8; ++i) f[i] = n + i < a.N ? f[i] : 0.0f;
+    }
     __bf16* q = (__bf16*)o + (long long)m * a.ldo + n;
     if (a.npl == 1) {
-        store_pack<__bf16, 4>(q, f, 4);
-    } else {
-        float s[3][4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float p[3];
-            split3(f[i], p);
-#pragma unroll
-            for (int k = 0; k < 3; ++k) s[k][i] = p[k];
-        }
-#pragma unroll
-        for (int k = 0; k < 3; ++k) store_pack<__bf16, 4>(q + k * a.plane, s[k], 4);
+        store_pack<__bf16, 8>(q, f, 8);
+        return;
     }
+    float s[3][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float p[3];
+        split3(f[i], p);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) s[k][i] = p[k];
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) store_pack<__bf16, 8>(q + k * a.plane, s[k], 8);
 }
 
-// Four consecutive columns into a result of the caller's layout.
+// Eight columns of row m into a result of the caller's layout.
 template <class T>
-__device__ __forceinline__ void store_out(const TileArgs& a, void* o, int m, int n, const float (&f)[4])
+__device__ __forceinline__ void store_out(const TileArgs& a, void* o, int m, int n, const float (&f)[8])
 {
     if (n >= a.N) return;
     T* r = (T*)o + (long long)m * a.ldo;
     const int q = n / a.oL, l = n - q * a.oL;
-    if (n + 4 <= a.N && l + 4 <= a.oL) {
-        store_pack<T, 4>(r + q * a.osb + l, f, 4);
+    if (n + 8 <= a.N && l + 8 <= a.oL) {
+        store_pack<T, 8>(r + q * a.osb + l, f, 8);
         return;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int c = n + i;
-        if (c >= a.N) break;
-        const int qq = c / a.oL;
-        r[qq * a.osb + (c - qq * a.oL)] = (T)f[i];
+    for (int i = 0; i < 8; ++i) {
+        const int c = n + i, qq = c / a.oL;
+        if (c < a.N) r[qq * a.osb + (c - qq * a.oL)] = (T)f[i];
     }
+}
+
+template <class Cfg, int EPI>
+constexpr int tile_lds()
+{
+    const int stages = 2 * (Cfg::kAB + Cfg::kBB), out = (EPI == kEpiGrad ? 3 : 2) * Sub<Cfg>::kBytes;
+    return stages > out ? stages : out;
 }
 
 template <class Cfg, bool BTR, int EPI>
 __global__ __launch_bounds__(Cfg::NTH) void k_ffn_tile(TileArgs a)
 {
-    __shared__ __align__(1024) char As[2 * Cfg::kAB];
-    __shared__ __align__(1024) char Bs[2 * Cfg::kBB];
-    const int tiles = a.tm * a.tn;
-    const int id = (int)blockIdx.x, s = id / tiles, tile = id - s * tiles;
-    const int m0 = (tile % a.tm) * (a.goff ? 2 * Cfg::BMG : Cfg::BMG), n0 = (tile / a.tm) * Cfg::BN;
+    __shared__ __align__(1024) char S[tile_lds<Cfg, EPI>()];
+    char *As = S, *Bs = S + 2 * Cfg::kAB;
+    // Workgroups are dealt to the eight XCDs in turn: each takes a contiguous run
+    // of tiles, in columns of up to kTileRows row tiles, so that the operands
+    // its workgroups share stay in its own L2.
+    const int G = (int)gridDim.x, xcd = (int)blockIdx.x & 7, per = G >> 3, rem = G & 7;
+    const int id = xcd * per + (xcd < rem ? xcd : rem) + ((int)blockIdx.x >> 3);
+    const int tiles = a.tm * a.tn, s = id / tiles, tile = id - s * tiles;
+    const int band = tile / (kTileRows * a.tn), in = tile - band * (kTileRows * a.tn);
+    const int left = a.tm - band * kTileRows, bm = left < kTileRows ? left : kTileRows;
+    const int m0 = (band * kTileRows + in % bm) * (a.goff ? 2 * Cfg::BMG : Cfg::BMG), n0 = (in / bm) * Cfg::BN;
     const int kb = s * a.kper, ke = kb + a.kper < a.K ? kb + a.kper : a.K;
     f32x16 acc[2][Cfg::MT][Cfg::NT] = {};
     tile_product<Cfg, 2, BTR>(a, 0, a.n1, a.ma, a.mb, a.K, kb, ke, m0, n0, As, Bs, acc);
@@ -328,63 +410,66 @@ __global__ __launch_bounds__(Cfg::NTH) void k_ffn_tile(TileArgs a)
         __syncthreads();
         tile_product<Cfg, 1, BTR>(a, a.n1, a.n2, a.ma2, a.mb2, a.K2, 0, a.K2, m0, n0, As, Bs, dh);
     }
-    const int t = (int)threadIdx.x, lane = t & 63, w = t >> 6, wm = w / Cfg::WN, wn = w % Cfg::WN;
+    typedef Sub<Cfg> E;
+    char *S0 = S, *S1 = S + E::kBytes, *S2 = S + 2 * E::kBytes;
 #pragma unroll
     for (int i = 0; i < Cfg::MT; ++i)
 #pragma unroll
-        for (int j = 0; j < Cfg::NT; ++j)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int m = m0 + (wm * Cfg::MT + i) * 32 + (lane & 31);
-                const int n = n0 + (wn * Cfg::NT + j) * 32 + 8 * q + 4 * (lane >> 5);
-                float f[2][4];
-#pragma unroll
-                for (int g = 0; g < 2; ++g)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) f[g][r] = acc[g][i][j][4 * q + r];
+        for (int j = 0; j < Cfg::NT; ++j) {
+            __syncthreads();
+            E::put(S0, acc[0][i][j]);
+            E::put(S1, acc[1][i][j]);
+            if constexpr (EPI == kEpiGrad) E::put(S2, dh[0][i][j]);
+            __syncthreads();
+            E::pieces([&](int row, int col) {
+                const int m = m0 + i * E::SR + row, n = n0 + j * E::SC + col;
+                float f0[8], f1[8];
+                E::get(S0, row, col, f0);
+                E::get(S1, row, col, f1);
                 if constexpr (EPI == kEpiOut || EPI == kEpiPart) {
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
                         const int mg = m + g * a.goff;
-                        if (mg >= a.M) continue;
+                        if (mg >= a.M) return;  // the second group's rows come after the first's
+                        const float(&f)[8] = g ? f1 : f0;
                         void* o = g && !a.goff ? a.o1 : a.o0;
-                        if constexpr (EPI == kEpiPart) {
-                            if (a.splits > 1) {
-                                // [piece][row][column], the second matrix's rows behind the first's
-                                float* d = (float*)a.o2 + ((long long)s * (a.goff ? a.M : 2 * a.M) + mg +
-                                                           (g && !a.goff ? a.M : 0)) * a.N + n;
-#pragma unroll
-                                for (int r = 0; r < 4; ++r)
-                                    if (n + r < a.N) d[r] = f[g][r];
-                                continue;
-                            }
+                        if (EPI == kEpiPart && a.splits > 1) {
+                            // [piece][row][column], the second matrix's rows behind the first's
+                            const int rows = a.goff ? a.M : 2 * a.M, at = g && !a.goff ? a.M : 0;
+                            store_out<float>(a, (float*)a.o2 + ((long long)s * rows + at) * a.N, mg, n, f);
+                        } else if (a.out32) {
+                            store_out<float>(a, o, mg, n, f);
+                        } else {
+                            store_out<__bf16>(a, o, mg, n, f);
                         }
-                        if (a.out32) store_out<float>(a, o, mg, n, f[g]);
-                        else store_out<__bf16>(a, o, mg, n, f[g]);
                     }
-                } else if constexpr (EPI == kEpiGate) {
-                    if (m >= a.M) continue;
-                    float hv[4];
+                } else if (m < a.M) {
+                    if constexpr (EPI == kEpiGate) {
+                        with_act(a.act, [&](auto act) {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) hv[r] = act_fwd(a.act, f[0][r]) * f[1][r];
-                    store_plane(a, a.o0, m, n, hv);
-                } else {
-                    if (m >= a.M) continue;
-                    float hv[4], dg[4], du[4];
+                            for (int r = 0; r < 8; ++r) f0[r] = act_fwd(act, f0[r]) * f1[r];
+                        });
+                        store_plane(a, a.o0, m, n, f0);
+                    } else {
+                        float d[8], du[8];
+                        E::get(S2, row, col, d);
+                        with_act(a.act, [&](auto act) {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        float ga, da;
-                        act_both(a.act, f[0][r], ga, da);
-                        const float d = dh[0][i][j][4 * q + r];
-                        hv[r] = ga * f[1][r];
-                        dg[r] = d * f[1][r] * da;
-                        du[r] = d * ga;
+                            for (int r = 0; r < 8; ++r) {
+                                float ga, da;
+                                act_both(act, f0[r], ga, da);
+                                f0[r] = ga * f1[r];
+                                du[r] = d[r] * ga;
+                                f1[r] = d[r] * f1[r] * da;
+                            }
+                        });
+                        store_plane(a, a.o0, m, n, f0);
+                        store_plane(a, a.o1, m, n, f1);
+                        store_plane(a, a.o2, m, n, du);
                     }
-                    store_plane(a, a.o0, m, n, hv);
-                    store_plane(a, a.o1, m, n, dg);
-                    store_plane(a, a.o2, m, n, du);
                 }
-            }
+            });
+        }
 }
 
 }  // namespace

@@ -94,6 +94,15 @@ constexpr int kCUs = 256;
 
 long long round8(long long v) { return (v + 7) & ~7ll; }
 
+// Row stride of the position planes: an odd multiple of 128 bytes, so that the
+// rows a stage reads (one column block of 64 rows) lie on different memory
+// channels whatever the number of positions.
+long long spread(long long v)
+{
+    const long long lines = (v + 63) / 64;
+    return (lines | 1) * 64;
+}
+
 // A packed operand or intermediate: planes of [rows][ld].
 struct Planes {
     __bf16* p;
@@ -149,7 +158,7 @@ Layout layout(int B, int C, int F, long long L, bool bf16, bool bwd)
     Layout o{};
     o.npl = bf16 ? 1 : 3;
     o.T = B * L;
-    o.Tp = round8(o.T);
+    o.Tp = spread(o.T);
     o.Cp = round8(C);
     o.Fp = round8(F);
     o.xdirect = bf16 && L % 8 == 0;
