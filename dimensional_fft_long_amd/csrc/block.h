@@ -52,6 +52,21 @@ struct FfnArgs {
     bool bf16;
 };
 
+// The one-launch forward for few channels (bf16, C <= kFusedMaxC): operands in
+// rows of 16-byte multiples, x and y as in FfnArgs or packed.
+constexpr int kFusedMaxC = 128;
+struct FusedFfn {
+    const void *x, *wg, *wu, *wd;
+    void* y;
+    long long ldx, sbx;  // x: element (c, n) at c ldx + (n / Lx) sbx + n % Lx
+    int Lx;
+    long long ldw, ldd;  // row strides of Wg / Wu and Wd
+    int C, F, N, act;
+    long long ldo, osb;  // y likewise
+    int oL;
+};
+hipError_t launch_ffn_fused(const FusedFfn& f, hipStream_t st);
+
 size_t ffn_workspace(int B, int C, int F, long long L, bool bf16, bool bwd);
 hipError_t launch_ffn_fwd(const FfnArgs& a, hipStream_t st);
 hipError_t launch_ffn_bwd(const FfnArgs& a, hipStream_t st);

@@ -103,7 +103,7 @@ __device__ __forceinline__ float act_fwd(int act, float v)
 {
     if (act == kActNone) return v;
     if (act == kActGelu) return 0.5f * v * (1.0f + erff(v * 0.707106781186547524f));
-    const float s = __builtin_amdgcn_rcpf(1.0f + exp_neg(v));
+    const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-v * kLog2e));
     return act == kActSilu ? v * s : s;
 }
 

@@ -317,6 +317,9 @@ struct Chain {
             (e = weight(f.Wu, o.wu, f.F, f.C, &wu, &mw)) != hipSuccess ||
             (e = weight(f.Wd, o.wd, f.C, f.F, &wd, &md)) != hipSuccess)
             return e;
+        if (f.bf16 && f.C <= kFusedMaxC)
+            return launch_ffn_fused(FusedFfn{x.p, wg.p, wu.p, wd.p, f.y, mx.ld, mx.sb, mx.L, mw.ld, md.ld, f.C, f.F,
+                                             (int)o.T, f.act, f.L, f.C * f.L, (int)f.L}, st);
         TileArgs a = base(f.F, o.T, f.C);
         a.n1 = add_phases(a, 0, o.npl, wg.p, wu.p, wg.plane, x.p, x.plane);
         a.ma = mw;
