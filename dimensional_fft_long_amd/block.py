@@ -21,13 +21,13 @@ while the stream is being captured, one of the graph's own memory.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (OK, HyenandError, _cached_ws, _check_out, _dims_arr, _dtype_code, _ws_bytes, get_lib)
+from . import (OK, HyenandError, _check_out, _dims_arr, _dtype_code, _ws_bytes, _ws_cache, get_lib)
 
 ACTS = {"none": 0, "sigmoid": 1, "silu": 2, "gelu": 3}
 
@@ -77,7 +77,7 @@ def _x(t, name="x"):
 def _like(t, name, x, optional=False):
     if t is None and optional:
         return
-    if not isinstance(t, torch.Tensor) or t.dtype != x.dtype or t.device != x.device or not t.is_contiguous():
+    if not isinstance(t, torch.Tensor) or t.dtype is not x.dtype or t.device != x.device or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous {x.dtype} tensor on {x.device}")
     if t.shape != x.shape:
         raise ValueError(f"{name} must have the shape {tuple(x.shape)}, got {tuple(t.shape)}")
@@ -86,8 +86,8 @@ def _like(t, name, x, optional=False):
 def _channel(t, name, x, optional=False):
     if t is None and optional:
         return
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.device != x.device or \
-            not t.is_contiguous() or tuple(t.shape) != (x.shape[1],):
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or t.device != x.device or \
+            not t.is_contiguous() or t.dim() != 1 or t.shape[0] != x.shape[1]:
         raise TypeError(f"{name} must be a contiguous float32 tensor of {x.shape[1]} elements on {x.device}")
 
 
@@ -111,40 +111,54 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _shape(x):
-    dims = tuple(int(v) for v in x.shape[2:])
-    return int(x.shape[0]), int(x.shape[1]), len(dims), _dims_arr(dims)
+@functools.lru_cache(maxsize=1024)
+def _shape(shape):
+    """(B, C, d, extents) of a tensor's shape, as the entry points take them."""
+    dims = tuple(int(v) for v in shape[2:])
+    return int(shape[0]), int(shape[1]), len(dims), _dims_arr(dims)
 
 
-@contextlib.contextmanager
-def _on(device, stream, inputs=()):
-    """The tensors' device and the call's stream made current, so that outputs
-    and workspaces come from that stream's memory; inputs of another stream are
-    marked as used on it."""
+# The current stream's handle; the public call builds a Stream object for it,
+# which costs as much as a small kernel.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _call(device, stream, inputs, body):
+    """body(stream handle) with the tensors' device and the call's stream
+    current, so that outputs and workspaces come from that stream's memory;
+    inputs of another stream are marked as used on it."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return body(_raw_stream(device.index))
     with torch.cuda.device(device):
         if stream is None:
-            yield _P(torch.cuda.current_stream(device).cuda_stream)
-            return
+            return body(_raw_stream(device.index))
         if stream.device != device:
             raise ValueError(f"the stream must be one of {device}, got {stream.device}")
         foreign = stream != torch.cuda.current_stream(device)
         with torch.cuda.stream(stream):
-            yield _P(stream.cuda_stream)
+            r = body(stream.cuda_stream)
             if foreign and not torch.cuda.is_current_stream_capturing():
                 for t in inputs:
                     if t is not None and t.numel():
                         t.record_stream(stream)
+    return r
 
 
-def _ws(workspace, kind, nbytes, device):
-    """(buffer, bytes): the caller's workspace, or one of the cache.  A captured
-    call takes memory of its graph instead: a cached buffer would be shared with
-    other graphs and with eager calls, which a replay does not wait for."""
+def _ws(workspace, kind, nbytes, device, st):
+    """(buffer, bytes): the caller's workspace, or one of the cache, one per kind,
+    device, size and stream.  A captured call takes memory of its graph instead:
+    a cached buffer would be shared with other graphs and with eager calls, which
+    a replay does not wait for."""
     if workspace is not None:
         return workspace, _ws_bytes(workspace, device)
     if torch.cuda.is_current_stream_capturing():
         return torch.empty(max(nbytes, 8), dtype=torch.uint8, device=device), nbytes
-    return _cached_ws(kind, nbytes, device, None)
+    key = (kind, device.index, nbytes, st)
+    buf = _ws_cache.get(key)
+    if buf is None:
+        buf = _ws_cache[key] = torch.empty(max(nbytes, 8), dtype=torch.uint8, device=device)
+    return buf, nbytes
 
 
 def _done(rc, what):
@@ -156,9 +170,12 @@ def _out(t, name, like, inputs):
     """A caller's output (or a new one): shape and dtype of ``like``, apart from every input."""
     if t is None:
         return torch.empty_like(like)
+    _check_out(t, name, like.shape, like.dtype, like.device)
+    a0 = t.data_ptr()
+    a1 = a0 + t.numel() * t.element_size()
     for i in inputs:
-        if i is not None:
-            _check_out(t, name, like.shape, like.dtype, like.device, like=i)
+        if i is not None and a0 < i.data_ptr() + i.numel() * i.element_size() and i.data_ptr() < a1:
+            raise ValueError(f"{name} must not overlap the inputs or another output")
     return t
 
 
@@ -168,12 +185,14 @@ def block_norm_fwd(x, w, eps: float = 1e-6, h=None, stream=None):
     """h = x r w, r the reciprocal root mean square of x over its channels."""
     dt = _x(x)
     _channel(w, "w", x)
-    with _on(x.device, stream, (x, w)) as st:
-        h = _out(h, "h", x, (x, w))
-        B, C, d, dims = _shape(x)
-        _done(get_lib().hyenand_block_norm_fwd(_ptr(x), _ptr(w), _ptr(h), B, C, d, dims, dt, eps, st),
+
+    def body(st):
+        o = _out(h, "h", x, (x, w))
+        _done(get_lib().hyenand_block_norm_fwd(x.data_ptr(), w.data_ptr(), o.data_ptr(), *_shape(x.shape), dt, eps, st),
               "block_norm_fwd")
-    return h
+        return o
+
+    return _call(x.device, stream, (x, w), body)
 
 
 def block_norm_bwd(x, w, dh, eps: float = 1e-6, workspace=None, stream=None):
@@ -181,14 +200,16 @@ def block_norm_bwd(x, w, dh, eps: float = 1e-6, workspace=None, stream=None):
     dt = _x(x)
     _channel(w, "w", x)
     _like(dh, "dh", x)
-    with _on(x.device, stream, (x, w, dh)) as st:
-        B, C, d, dims = _shape(x)
+
+    def body(st):
+        lib, shape = get_lib(), _shape(x.shape)
         dx, dw = torch.empty_like(x), torch.empty_like(w)
-        ws, nb = _ws(workspace, "block_norm_bwd",
-                     get_lib().hyenand_block_norm_bwd_workspace_bytes(B, C, d, dims, dt), x.device)
-        _done(get_lib().hyenand_block_norm_bwd(_ptr(x), _ptr(w), _ptr(dh), _ptr(dx), _ptr(dw), B, C, d, dims, dt, eps,
-                                               _ptr(ws), nb, st), "block_norm_bwd")
-    return dx, dw
+        ws, nb = _ws(workspace, "block_norm_bwd", lib.hyenand_block_norm_bwd_workspace_bytes(*shape, dt), x.device, st)
+        _done(lib.hyenand_block_norm_bwd(x.data_ptr(), w.data_ptr(), dh.data_ptr(), dx.data_ptr(), dw.data_ptr(),
+                                         *shape, dt, eps, ws.data_ptr(), nb, st), "block_norm_bwd")
+        return dx, dw
+
+    return _call(x.device, stream, (x, w, dh), body)
 
 
 class BlockNormFunction(torch.autograd.Function):
@@ -234,14 +255,15 @@ def block_join_fwd(x, m, gate=None, scale=None, w_post=None, w_pre=None, gate_ac
     ins = (x, m, gate, scale, w_post, w_pre)
     if w_pre is None and h is not None:
         raise ValueError("h is computed only with w_pre")
-    with _on(x.device, stream, ins + (rng,)) as st:
-        out = _out(out, "out", x, ins)
-        if w_pre is not None:
-            h = _out(h, "h", x, ins + (out,))
-        B, C, d, dims = _shape(x)
-        _done(get_lib().hyenand_block_join_fwd(_ptr(x), _ptr(m), ctypes.byref(j), _ptr(out), _ptr(h), B, C, d, dims,
-                                               dt, st), "block_join_fwd")
-    return out, h
+
+    def body(st):
+        o = _out(out, "out", x, ins)
+        hh = None if w_pre is None else _out(h, "h", x, ins + (o,))
+        _done(get_lib().hyenand_block_join_fwd(x.data_ptr(), m.data_ptr(), ctypes.byref(j), o.data_ptr(), _ptr(hh),
+                                               *_shape(x.shape), dt, st), "block_join_fwd")
+        return o, hh
+
+    return _call(x.device, stream, ins + (rng,), body)
 
 
 def block_join_bwd(x, m, dout, dh, gate=None, scale=None, w_post=None, w_pre=None, gate_act: str = "sigmoid",
@@ -254,18 +276,19 @@ def block_join_bwd(x, m, dout, dh, gate=None, scale=None, w_post=None, w_pre=Non
     _like(dh, "dh", x, optional=True)
     if dh is not None and w_pre is None:
         raise ValueError("dh goes with w_pre")
-    with _on(x.device, stream, (x, m, dout, dh, gate, scale, w_post, w_pre, rng)) as st:
+
+    def body(st):
+        lib, shape = get_lib(), _shape(x.shape)
         g = {"dx": torch.empty_like(x), "dm": torch.empty_like(x)}
         for k, t in (("dgate", gate), ("dscale", scale), ("dw_post", w_post), ("dw_pre", w_pre)):
             g[k] = None if t is None else torch.empty_like(t)
-        B, C, d, dims = _shape(x)
-        ws, nb = _ws(workspace, "block_join_bwd",
-                     get_lib().hyenand_block_join_bwd_workspace_bytes(B, C, d, dims, dt), x.device)
-        gs = _JoinGrads(*(_ptr(g[k]) for k, _ in _JoinGrads._fields_))
-        _done(get_lib().hyenand_block_join_bwd(_ptr(x), _ptr(m), ctypes.byref(j), _ptr(dout), _ptr(dh),
-                                               ctypes.byref(gs), B, C, d, dims, dt, _ptr(ws), nb, st),
-              "block_join_bwd")
-    return g
+        ws, nb = _ws(workspace, "block_join_bwd", lib.hyenand_block_join_bwd_workspace_bytes(*shape, dt), x.device, st)
+        gs = _JoinGrads(*(_ptr(t) for t in g.values()))  # the structure's own order
+        _done(lib.hyenand_block_join_bwd(x.data_ptr(), m.data_ptr(), ctypes.byref(j), _ptr(dout), _ptr(dh),
+                                         ctypes.byref(gs), *shape, dt, ws.data_ptr(), nb, st), "block_join_bwd")
+        return g
+
+    return _call(x.device, stream, (x, m, dout, dh, gate, scale, w_post, w_pre, rng), body)
 
 
 class BlockJoinFunction(torch.autograd.Function):
@@ -304,10 +327,14 @@ def dropout_fwd(x, p: float, rng, y=None, stream=None):
         raise TypeError("x must be a contiguous device tensor")
     dt = _dtype_code(x.dtype)
     p = _rng(rng, p, x.device)
-    with _on(x.device, stream, (x, rng)) as st:
-        y = _out(y, "y", x, (x,))
-        _done(get_lib().hyenand_dropout(_ptr(x), _ptr(y), x.numel(), dt, p, _ptr(rng) if p else None, st), "dropout")
-    return y
+
+    def body(st):
+        o = _out(y, "y", x, (x,))
+        _done(get_lib().hyenand_dropout(x.data_ptr(), o.data_ptr(), x.numel(), dt, p, _ptr(rng) if p else None, st),
+              "dropout")
+        return o
+
+    return _call(x.device, stream, (x, rng), body)
 
 
 def dropout_bwd(dy, p: float, rng, dx=None, stream=None):
@@ -364,29 +391,34 @@ def gated_ffn_fwd(x, Wg, Wu, Wd, act: str = "silu", y=None, workspace=None, stre
     """y = Wd (act(Wg x) * (Wu x)) at every position; Wg, Wu [F, C], Wd [C, F]
     of x's dtype, 16-byte aligned like x."""
     dt, F, a = _ffn(x, Wg, Wu, Wd, act)
-    with _on(x.device, stream, (x, Wg, Wu, Wd)) as st:
-        y = _out(y, "y", x, (x, Wg, Wu, Wd))
-        B, C, d, dims = _shape(x)
-        ws, nb = _ws(workspace, "gated_ffn",
-                     get_lib().hyenand_gated_ffn_workspace_bytes(B, C, F, d, dims, dt), x.device)
-        _done(get_lib().hyenand_gated_ffn_fwd(_ptr(x), _ptr(Wg), _ptr(Wu), _ptr(Wd), _ptr(y), B, C, F, d, dims, dt, a,
-                                              _ptr(ws), nb, st), "gated_ffn_fwd")
-    return y
+
+    def body(st):
+        lib, (B, C, d, dims) = get_lib(), _shape(x.shape)
+        o = _out(y, "y", x, (x, Wg, Wu, Wd))
+        ws, nb = _ws(workspace, "gated_ffn", lib.hyenand_gated_ffn_workspace_bytes(B, C, F, d, dims, dt), x.device, st)
+        _done(lib.hyenand_gated_ffn_fwd(x.data_ptr(), Wg.data_ptr(), Wu.data_ptr(), Wd.data_ptr(), o.data_ptr(), B, C, F,
+                                        d, dims, dt, a, ws.data_ptr(), nb, st), "gated_ffn_fwd")
+        return o
+
+    return _call(x.device, stream, (x, Wg, Wu, Wd), body)
 
 
 def gated_ffn_bwd(x, Wg, Wu, Wd, dy, act: str = "silu", workspace=None, stream=None):
     """(dx, dWg, dWu, dWd) of gated_ffn_fwd for the gradient dy of y."""
     dt, F, a = _ffn(x, Wg, Wu, Wd, act)
     _like(dy, "dy", x)
-    with _on(x.device, stream, (x, Wg, Wu, Wd, dy)) as st:
+
+    def body(st):
+        lib, (B, C, d, dims) = get_lib(), _shape(x.shape)
         dx, dWg, dWu, dWd = (torch.empty_like(t) for t in (x, Wg, Wu, Wd))
-        B, C, d, dims = _shape(x)
-        ws, nb = _ws(workspace, "gated_ffn_bwd",
-                     get_lib().hyenand_gated_ffn_bwd_workspace_bytes(B, C, F, d, dims, dt), x.device)
-        _done(get_lib().hyenand_gated_ffn_bwd(_ptr(x), _ptr(Wg), _ptr(Wu), _ptr(Wd), _ptr(dy), _ptr(dx), _ptr(dWg),
-                                              _ptr(dWu), _ptr(dWd), B, C, F, d, dims, dt, a, _ptr(ws), nb, st),
-              "gated_ffn_bwd")
-    return dx, dWg, dWu, dWd
+        ws, nb = _ws(workspace, "gated_ffn_bwd", lib.hyenand_gated_ffn_bwd_workspace_bytes(B, C, F, d, dims, dt),
+                     x.device, st)
+        _done(lib.hyenand_gated_ffn_bwd(x.data_ptr(), Wg.data_ptr(), Wu.data_ptr(), Wd.data_ptr(), dy.data_ptr(),
+                                        dx.data_ptr(), dWg.data_ptr(), dWu.data_ptr(), dWd.data_ptr(), B, C, F, d, dims,
+                                        dt, a, ws.data_ptr(), nb, st), "gated_ffn_bwd")
+        return dx, dWg, dWu, dWd
+
+    return _call(x.device, stream, (x, Wg, Wu, Wd, dy), body)
 
 
 class GatedFFNFunction(torch.autograd.Function):

@@ -3,6 +3,7 @@
 // and error mapping.
 #include <hip/hip_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 
 #include "../../include/hyenand.h"
@@ -47,9 +48,10 @@ int common(int B, int C, int d, const int64_t* dims, int dtype, long long* L)
     return HYENAND_OK;
 }
 
+// A normal positive number: the hardware's reciprocal square root takes no others.
 int checked_eps(float eps)
 {
-    return eps > 0.0f && std::isfinite(eps) ? HYENAND_OK : HYENAND_ERR_INVALID_ARG;
+    return eps >= FLT_MIN && std::isfinite(eps) ? HYENAND_OK : HYENAND_ERR_INVALID_ARG;
 }
 
 // Dropout probability and generator; p = 0 draws nothing.

@@ -67,6 +67,10 @@ struct FusedFfn {
 };
 hipError_t launch_ffn_fused(const FusedFfn& f, hipStream_t st);
 
+// The forward for few positions, straight from the caller's weights.
+constexpr int kFewPositions = 64;
+hipError_t launch_ffn_few(const FfnArgs& a, hipStream_t st);
+
 size_t ffn_workspace(int B, int C, int F, long long L, bool bf16, bool bwd);
 hipError_t launch_ffn_fwd(const FfnArgs& a, hipStream_t st);
 hipError_t launch_ffn_bwd(const FfnArgs& a, hipStream_t st);

@@ -95,12 +95,13 @@ __device__ __forceinline__ float exp_neg(float v)
     return __builtin_amdgcn_exp2f(t);
 }
 
-enum { kActNone = 0, kActSigmoid = 1, kActSilu = 2, kActGelu = 3 };
+enum { kActNone = 0, kActSigmoid = 1, kActSilu = 2, kActGelu = 3, kActOne = 4 };  // One: no gate at all
 
 // Activation a(v) and its derivative.  1 - s is taken as exp(-v) s, which keeps
 // its relative accuracy where s rounds to one.
 __device__ __forceinline__ float act_fwd(int act, float v)
 {
+    if (act == kActOne) return 1.0f;
     if (act == kActNone) return v;
     if (act == kActGelu) return 0.5f * v * (1.0f + erff(v * 0.707106781186547524f));
     const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-v * kLog2e));
@@ -109,6 +110,11 @@ __device__ __forceinline__ float act_fwd(int act, float v)
 
 __device__ __forceinline__ void act_both(int act, float v, float& a, float& da)
 {
+    if (act == kActOne) {
+        a = 1.0f;
+        da = 0.0f;
+        return;
+    }
     if (act == kActNone) {
         a = v;
         da = 1.0f;
@@ -136,7 +142,16 @@ __device__ __forceinline__ void with_act(int act, F&& f)
 {
     if (act == kActSilu) f(std::integral_constant<int, kActSilu>{});
     else if (act == kActSigmoid) f(std::integral_constant<int, kActSigmoid>{});
-    else if (act == kActGelu) f(std::integral_constant<int, kActGelu>{});
+    else f(std::integral_constant<int, kActGelu>{});
+}
+
+// The same for a join's gate.
+template <class F>
+__device__ __forceinline__ void with_gate(bool gate, int act, F&& f)
+{
+    if (!gate) f(std::integral_constant<int, kActOne>{});
+    else if (act == kActSigmoid) f(std::integral_constant<int, kActSigmoid>{});
+    else if (act == kActSilu) f(std::integral_constant<int, kActSilu>{});
     else f(std::integral_constant<int, kActNone>{});
 }
 
@@ -164,23 +179,26 @@ __device__ __forceinline__ void random4(unsigned long long key, unsigned long lo
 
 // Keep bits of the V consecutive elements from linear index e0 on: bit v set
 // iff element e0 + v is kept.  Element e takes word e % 4 of the block at
-// counter offset + e / 4.
+// counter offset + e / 4.  `whole` (the same for all lanes): no group of four
+// reaches past ceil(V / 4) blocks, the case of rows that are multiples of four.
 template <int V>
 __device__ __forceinline__ unsigned keep_bits(unsigned long long seed, unsigned long long offset, unsigned thr,
-                                              unsigned long long e0)
+                                              unsigned long long e0, bool whole)
 {
     const unsigned sh = (unsigned)e0 & 3u;
     const unsigned long long q = offset + (e0 >> 2);
-    unsigned bits = 0;
     constexpr int G = (V + 3) / 4;
-#pragma unroll
-    for (int g = 0; g <= G; ++g) {
-        // The last group is reached only by an unaligned start.
-        if (g == G && sh + V <= 4u * G) break;
+    unsigned bits = 0;
+    const auto block = [&](int g) {
         unsigned w[4];
         random4(seed, q + g, w);
 #pragma unroll
         for (int j = 0; j < 4; ++j) bits |= (w[j] >= thr ? 1u : 0u) << (4 * g + j);
+    };
+#pragma unroll
+    for (int g = 0; g < G; ++g) block(g);
+    if constexpr (V > 1) {
+        if (!whole) block(G);
     }
     return bits >> sh;
 }

@@ -1,0 +1,284 @@
+// k_block_bwd.hip -- the norm and the join, backward.
+//
+// Measured on one MI355X: norm of 2 x 1024 x 16384 bf16 (three tensors) 97 us,
+// 2.1 TB/s; join of 2 x 128 x 1024^2 bf16 (eight tensors) 2.0 ms, 2.1 TB/s.  The
+// join issues 133 vector instructions an element (46% of the issue slots) and
+// its waves wait for 67% of their cycles: four waves a SIMD of 128 registers
+// are what the five tensors leave, with three sums (each behind two barriers)
+// a tile between the loads and the stores.
+#include "block_tile.h"
+
+namespace hyenand {
+namespace {
+
+// Backward.  With n = m r_m w_post, b = s a(gate) n up keep, out = x + b and
+// h = out r_o w_pre:
+//   do  = dout + r_o dn - out r_o^3 mean_c(dn out),  dn = dh w_pre
+//   dx  = do,  db = do up keep,  dgate = db s n a'
+//   e   = db s a,  dm = r_m e w_post - m r_m^3 mean_c(e w_post m)   (e without the post norm)
+//   Q_c = sum db a m r_m: dscale = w_post Q, dw_post = s Q;  dw_pre = sum dh out r_o
+// Both channel sums stay in registers over all of a workgroup's tiles and are
+// joined in a fixed order by k_block_reduce.
+template <class T, bool JOIN, int V, int K, bool ROW, int NT>
+__global__ __launch_bounds__(NT, NT == 1024 ? 4 : V * K <= (JOIN ? 8 : 16) ? 4 : 2) void k_block_bwd(BlockArgs a, Lay g)
+{
+    __shared__ __align__(16) float red[2 * red_floats(NT)];
+    int turn = 0;
+    const float invC = 1.0f / (float)a.C;
+    unsigned long long seed = 0, offs = 0;
+    const bool drop = JOIN && a.drop.rng;
+    if (drop) {
+        seed = a.drop.rng[0];
+        offs = a.drop.rng[1];
+    }
+    const float up = drop ? a.drop.up : 1.0f;
+    Params<V, K, ROW> sw, wpre;  // scale w_post, w_pre
+    {
+        const Where<V, ROW> w(a, g);  // channels only
+        if (JOIN) {
+            Params<V, K, ROW> sc;
+            sw.load(a.w_post, w, 1.0f);
+            sc.load(a.scale, w, 1.0f);
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int i = 0; i < (ROW ? V : 1); ++i) sw.v[k][i] *= sc.v[k][i];
+        }
+        wpre.load(a.w_pre, w, 0.0f);
+    }
+    constexpr int VA = ROW ? V : 1;
+    float Q[K][VA], S[K][VA];
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int v = 0; v < VA; ++v) Q[k][v] = S[k][v] = 0.0f;
+    Where<V, ROW> w(a, g);
+    for (long long tile = blockIdx.x; tile < g.tiles; tile += gridDim.x) {
+        w.at(a, g, tile);
+        Pack<T, V> xr[K], mr[JOIN ? K : 1], gr[JOIN ? K : 1], hr[K], dr[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            if (JOIN) mr[k] = load_group<T, V, ROW>(a.m, w, k);
+            if (a.dh) {
+                xr[k] = load_group<T, V, ROW>(a.x, w, k);
+                hr[k] = load_group<T, V, ROW>(a.dh, w, k);
+            }
+            if (JOIN && a.gate) gr[k] = load_group<T, V, ROW>(a.gate, w, k);
+        }
+        // Dropout's words while the loads are in flight.
+        unsigned keep[JOIN ? K : 1];
+        if (JOIN) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                keep[k] = ~0u;
+                if (drop) keep[k] = keep_bits<V>(seed, offs, a.drop.thr, (unsigned long long)w.off(k), g.whole4);
+            }
+        }
+        float rm[1][V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) rm[0][v] = 1.0f;
+        if (JOIN && a.w_post) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) rm[0][v] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    if (!ROW || w.mine(k, v)) rm[0][v] += mr[k].get(v) * mr[k].get(v);
+            sum_channels<1, V, ROW, NT>(rm, red, turn, g.lxs);
+#pragma unroll
+            for (int v = 0; v < V; ++v) rm[0][v] = __builtin_amdgcn_rsqf(rm[0][v] * invC + a.eps);
+        }
+        with_gate(JOIN && a.gate, a.act, [&](auto act) {
+            // out of element (k, v), computed where it is needed.
+            const auto out_at = [&](int k, int v) {
+                float val = xr[k].get(v);
+                if constexpr (JOIN) {
+                    const float b = sw.at(k, v) * act_fwd(act, gr[k].get(v)) * (mr[k].get(v) * rm[0][v]) * up;
+                    val += kept(keep[k], v, b);
+                }
+                return val;
+            };
+            // 0 for the positions that another lane counts, else 1.
+            float once[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) once[v] = ROW || v >= w.skip ? 1.0f : 0.0f;
+            float s2[2][V], ro[V], co[V];
+            if (a.dh) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) s2[0][v] = s2[1][v] = 0.0f;
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        const float val = out_at(k, v);
+                        if (!ROW || w.mine(k, v)) {
+                            s2[0][v] += val * val;
+                            s2[1][v] += hr[k].get(v) * wpre.at(k, v) * val;
+                        }
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                if (a.dout) dr[k] = load_group<T, V, ROW>(a.dout, w, k);
+                else dr[k] = Pack<T, V>{};
+            }
+            if (a.dh) {
+                sum_channels<2, V, ROW, NT>(s2, red, turn, g.lxs);
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    ro[v] = __builtin_amdgcn_rsqf(s2[0][v] * invC + a.eps);
+                    co[v] = ro[v] * ro[v] * ro[v] * (s2[1][v] * invC);
+                }
+            }
+            float ev[JOIN ? K : 1][V], em[1][V];  // e w_post
+#pragma unroll
+            for (int v = 0; v < V; ++v) em[0][v] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                float dv[V], dg[V];
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    dv[v] = dr[k].get(v);
+                    if (a.dh) {
+                        const float dhr = hr[k].get(v) * ro[v], val = out_at(k, v);
+                        dv[v] += dhr * wpre.at(k, v) - val * co[v];
+                        S[k][ROW ? v : 0] += dhr * val * once[v];
+                    }
+                }
+                store_group<T, V, ROW>(a.dx, w, k, dv);
+                if constexpr (JOIN) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        float ga, da;
+                        act_both(act, gr[k].get(v), ga, da);
+                        const float db = kept(keep[k], v, dv[v] * up);
+                        const float mn = mr[k].get(v) * rm[0][v], dbs = db * sw.at(k, v);
+                        dg[v] = dbs * mn * da;
+                        ev[k][v] = dbs * ga;
+                        Q[k][ROW ? v : 0] += db * ga * mn * once[v];
+                        if (!ROW || w.mine(k, v)) em[0][v] += ev[k][v] * mr[k].get(v);
+                    }
+                    if (act != kActOne) store_group<T, V, ROW>(a.dgate, w, k, dg);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if constexpr (JOIN) {
+                if (a.w_post) {
+                    sum_channels<1, V, ROW, NT>(em, red, turn, g.lxs);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) em[0][v] *= rm[0][v] * rm[0][v] * rm[0][v] * invC;
+                }
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    if (a.w_post) {
+#pragma unroll
+                        for (int v = 0; v < V; ++v) ev[k][v] = ev[k][v] * rm[0][v] - mr[k].get(v) * em[0][v];
+                    }
+                    store_group<T, V, ROW>(a.dm, w, k, ev[k]);
+                }
+            }
+        });
+    }
+    // Partial sums of this workgroup's tiles.
+    float* part = a.part + (long long)blockIdx.x * 2 * a.C;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+#pragma unroll
+        for (int v = 0; v < VA; ++v) {
+            float q = Q[k][v], s = S[k][v];
+            if constexpr (!ROW) {
+                for (int of = 1; of < (1 << g.lxs); of <<= 1) {
+                    q += __shfl_xor(q, of);
+                    s += __shfl_xor(s, of);
+                }
+                if ((int)threadIdx.x & ((1 << g.lxs) - 1)) continue;
+            }
+            if (w.cy + k * w.step < a.C) {
+                part[w.chan(k, v)] = q;
+                part[a.C + w.chan(k, v)] = s;
+            }
+        }
+    }
+}
+
+// Channel gradients from the workgroups' partial sums, in double and in a fixed
+// order: 16 channels by 64 groups of workgroups.
+__global__ __launch_bounds__(1024) void k_block_reduce(BlockArgs a, int parts)
+{
+    __shared__ double R[2][64][16];
+    const int lc = (int)threadIdx.x & 15, gr = (int)threadIdx.x >> 4, c = (int)blockIdx.x * 16 + lc;
+    double q = 0.0, s = 0.0;
+    if (c < a.C)
+        for (int p = gr; p < parts; p += 64) {
+            const float* r = a.part + (long long)p * 2 * a.C;
+            q += (double)r[c];
+            s += (double)r[a.C + c];
+        }
+    R[0][gr][lc] = q;
+    R[1][gr][lc] = s;
+    __syncthreads();
+    for (int h = 32; h > 0; h >>= 1) {
+        if (gr < h) {
+            R[0][gr][lc] += R[0][gr + h][lc];
+            R[1][gr][lc] += R[1][gr + h][lc];
+        }
+        __syncthreads();
+    }
+    if (gr == 0 && c < a.C) {
+        const double Q = R[0][0][lc];
+        if (a.dscale) a.dscale[c] = (float)(a.w_post ? Q * (double)a.w_post[c] : Q);
+        if (a.dw_post) a.dw_post[c] = (float)(a.scale ? Q * (double)a.scale[c] : Q);
+        if (a.dw_pre) a.dw_pre[c] = (float)R[1][0][lc];
+    }
+}
+
+template <class T, bool JOIN, int V, int K, bool ROW, int NT>
+hipError_t run(const BlockArgs& a, const Shape& s, hipStream_t st)
+{
+    const unsigned grid = (unsigned)(s.g.tiles < kBlockMaxParts ? s.g.tiles : kBlockMaxParts);
+    hipLaunchKernelGGL((k_block_bwd<T, JOIN, V, K, ROW, NT>), dim3(grid), dim3(s.nt), 0, st, a, s.g);
+    const hipError_t e = launch_status();
+    if (e != hipSuccess || !(a.dscale || a.dw_post || a.dw_pre)) return e;
+    hipLaunchKernelGGL(k_block_reduce, dim3((a.C + 15) / 16), dim3(1024), 0, st, a, (int)grid);
+    return launch_status();
+}
+
+template <class T, bool JOIN>
+hipError_t dispatch(const BlockArgs& a, hipStream_t st)
+{
+    // The join holds five tensors: four elements a lane and workgroups of 1024
+    // threads keep two groups of channels within 128 registers on 128-byte rows
+    // (bf16; eight elements a lane spill: 2.0 against 2.5 ms at 2 x 128 x 1024^2).
+    constexpr int F = 16 / (int)sizeof(T), V = JOIN ? 4 : F, NT = JOIN ? 1024 : 512;
+    const Shape s = JOIN ? pick(a, V, NT, 2, 4) : pick(a, V, NT, 4, 8);
+    if (s.row) {
+        if (s.K == 1) return run<T, JOIN, F, 1, true, 512>(a, s, st);
+        if (s.K == 2) return run<T, JOIN, F, 2, true, 512>(a, s, st);
+        return run<T, JOIN, F, 4, true, 512>(a, s, st);
+    }
+    if (s.V > 1) {
+        if (s.K == 1) return run<T, JOIN, V, 1, false, NT>(a, s, st);
+        if (s.K == 2) return run<T, JOIN, V, 2, false, NT>(a, s, st);
+        if (s.K == 4) return run<T, JOIN, V, 4, false, NT>(a, s, st);
+        if (JOIN || s.K == 8) return run<T, JOIN, V, 8, false, NT>(a, s, st);  // the join: 8192 channels at most
+        if constexpr (!JOIN) return run<T, JOIN, V / 2, 16, false, NT>(a, s, st);
+    }
+    if (s.K == 1) return run<T, JOIN, 1, 1, false, 512>(a, s, st);
+    if (s.K == 2) return run<T, JOIN, 1, 2, false, 512>(a, s, st);
+    if (s.K == 4) return run<T, JOIN, 1, 4, false, 512>(a, s, st);
+    if (s.K == 8) return run<T, JOIN, 1, 8, false, 512>(a, s, st);
+    return run<T, JOIN, 1, 16, false, 512>(a, s, st);
+}
+
+}  // namespace
+
+hipError_t launch_block_bwd(const BlockArgs& a, hipStream_t st)
+{
+    if (a.m) return a.bf16 ? dispatch<__bf16, true>(a, st) : dispatch<float, true>(a, st);
+    return a.bf16 ? dispatch<__bf16, false>(a, st) : dispatch<float, false>(a, st);
+}
+
+}  // namespace hyenand

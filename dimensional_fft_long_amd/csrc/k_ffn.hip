@@ -421,7 +421,12 @@ hipError_t launch_ffn_zero(void* p, long long bytes, hipStream_t st)
 
 size_t ffn_workspace(int B, int C, int F, long long L, bool bf16, bool bwd) { return layout(B, C, F, L, bf16, bwd).total; }
 
-hipError_t launch_ffn_fwd(const FfnArgs& a, hipStream_t st) { return Chain(a, false, st).forward(); }
+hipError_t launch_ffn_fwd(const FfnArgs& a, hipStream_t st)
+{
+    if (a.B * a.L <= kFewPositions) return launch_ffn_few(a, st);
+    return Chain(a, false, st).forward();
+}
+
 hipError_t launch_ffn_bwd(const FfnArgs& a, hipStream_t st) { return Chain(a, true, st).backward(); }
 
 }  // namespace hyenand

@@ -432,7 +432,8 @@ int hyenand_fftconv_fwd_noalloc(const void* x, const float* phi_alpha, const flo
 /*
  * The norm ahead of a block, over the channels:
  *     r[b,i] = (mean_c x[b,c,i]^2 + eps)^(-1/2),   h[b,c,i] = x[b,c,i] r[b,i] w[c].
- * x, h: device [B][C][dims] of `dtype`; w: device fp32 [C]; eps > 0, finite.
+ * x, h: device [B][C][dims] of `dtype`; w: device fp32 [C]; eps a positive normal
+ * fp32 number.
  * C <= 8192 (else UNSUPPORTED).  No workspace.
  * Errors: INVALID_ARG, UNSUPPORTED, HIP.
  */

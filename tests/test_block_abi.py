@@ -49,7 +49,7 @@ def test_norm_refusals(H):
         assert b(**{k: None}) == 1 and b(**{k: ODD}) == 1, k
     for g in (f, b):
         assert g(B=-1) == 1 and g(C=-1) == 1 and g(dt=2) == 1 and g(dims=None) == 1 and g(C=8193) == 2
-        for eps in (0.0, -1e-6, math.inf, math.nan):
+        for eps in (0.0, -1e-6, 1e-40, math.inf, math.nan):
             assert g(eps=eps) == 1
         for d, dims, code in SHAPES:
             assert g(d=d, dims=_dims(*dims)) == code, dims
@@ -101,7 +101,7 @@ def test_join_refusals(H):
             assert q(**{k: 0x10001}) == 1, k
         for act in (-1, 3, 7):
             assert q(gate_act=act) == 1
-        for eps in (0.0, math.nan, math.inf):
+        for eps in (0.0, 1e-40, math.nan, math.inf):
             assert q(eps=eps) == 1
         for p in (-0.1, 1.0, 2.0, math.nan):
             assert q(p=p) == 1
