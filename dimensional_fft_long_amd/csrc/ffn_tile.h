@@ -9,16 +9,18 @@
 // consecutive k of a column into a lane, so activations are used where they lie.
 //
 // fp32 operands come as three bf16 planes whose sum is the value (8 bits each,
-// split by truncation: exact, and the leading plane cannot overflow).  A product
-// of two such sums runs as six phases over pairs of planes, smallest first,
-// into the same fp32 accumulators; the three pairs left out are below 2^-23 of
-// |a| |b|.  Six bf16 phases have 2.7 times the rate of the fp32 matrix
+// split by truncation: exact, and the leading plane cannot overflow).  A step
+// reads the three planes of both operands once and multiplies six pairs of
+// them; the three pairs left out are below 2^-23 of |a| |b|.  The leading pair
+// has an accumulator of its own, so the five small ones do not add to its
+// roundings.  Six bf16 products have 2.7 times the rate of the fp32 matrix
 // instruction (2.5 / 6 against 0.157 PFLOP/s).
 //
-// Pipeline: two LDS stages of 64 terms.  Loads go from global memory straight
-// to LDS (16 bytes a lane) one stage ahead, so a stage has the whole product of
-// the stage before to arrive; one barrier per stage.
+// Pipeline: NST LDS stages of BK terms, filled from global memory directly (16
+// bytes a lane) NST - 1 stages ahead; one barrier per stage.
 #pragma once
+
+#include <type_traits>
 
 #include "block_dev.h"
 
@@ -28,8 +30,8 @@ namespace {
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kBK = 64;          // terms of a stage
-constexpr int kMaxPhases = 12;
+constexpr int kPiece = 64;       // pieces of K (weight gradients) are multiples of this
+constexpr int kMaxPhases = 3;
 constexpr int kTileRows = 8;     // row tiles of a band
 
 __device__ __align__(16) const unsigned g_zeros[4] = {0, 0, 0, 0};
@@ -37,41 +39,43 @@ __device__ __align__(16) const unsigned g_zeros[4] = {0, 0, 0, 0};
 // k-contiguous rows: element (r, k) at r * ld + (k / L) * sb + k % L (L: the
 // positions of a batch entry, or more than K for one piece).
 // Column-contiguous (B only): element (k, n) at k * ld + (n / L) * sb + n % L.
+// plane: distance of the planes of fp32.
 struct Mat {
-    long long ld, sb;
+    long long ld, sb, plane;
     int L;
 };
 
 struct TileArgs {
-    // Phase p adds A[p][g] B[p] to row group g of the accumulators; phases from
-    // n1 on (gradient epilogue) to the third group, with K2 terms.
+    // Phase p adds A[p][g] B[p] to row group g of the accumulators; phase n1 (of
+    // the gradient epilogue) adds to the third group, with K2 terms.
     const __bf16 *A0[kMaxPhases], *A1[kMaxPhases], *B[kMaxPhases];
-    int n1, n2;
+    int n1;
     Mat ma, mb, ma2, mb2;
     int M, N, K, K2;
     int goff;            // rows between the two groups (0: two matrices of the same rows)
     int tm, tn, splits;  // tiles along M and N, pieces of K
-    int kper;            // terms of a piece (a multiple of kBK)
+    int kper;            // terms of a piece
     // outputs
     void *o0, *o1, *o2;  // stored rows; planes: first plane of each
     long long ldo, osb;  // row stride, batch stride of the output
     int oL;              // positions of a batch entry of the output
     long long plane;     // distance of the planes of an output
-    int npl;             // planes written (1 or 3)
     int act;
     bool out32;          // fp32 output (else bf16)
 };
 
 enum { kEpiOut = 0, kEpiGate = 1, kEpiGrad = 2, kEpiPart = 3 };
 
-template <int WM_, int WN_, int MT_, int NT_>
+template <int WM_, int WN_, int MT_, int NT_, int BK_, int NST_, int NPL_>
 struct TileCfg {
-    static constexpr int WM = WM_, WN = WN_, MT = MT_, NT = NT_;
+    static constexpr int WM = WM_, WN = WN_, MT = MT_, NT = NT_, BK = BK_, NST = NST_, NPL = NPL_;
     static constexpr int NTH = 64 * WM * WN;
     static constexpr int BMG = 32 * WM * MT;  // rows of a group
     static constexpr int BN = 32 * WN * NT;
-    static constexpr int kAB = 2 * BMG * kBK * 2, kBB = BN * kBK * 2;  // bytes of a stage
-    static constexpr int NA = 2 * BMG * 8 / NTH, NB = BN * 8 / NTH;    // 16-byte pieces a thread loads per stage
+    static constexpr int PR = BK / 8;         // 16-byte pieces of a k-contiguous row
+    static constexpr int kA1 = 2 * BMG * BK * 2, kB1 = BN * BK * 2;  // bytes of a plane's tile
+    static constexpr int kStage = NPL * (kA1 + kB1);
+    static constexpr int NACC = NPL == 1 ? 1 : 2;  // accumulators: the leading pair's, the small pairs'
 };
 
 typedef __attribute__((address_space(3))) void lds_void;
@@ -86,95 +90,137 @@ __device__ __forceinline__ void to_lds(const void* g, unsigned l)
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(l), "v"(g) : "memory");
 }
 
-__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// All but the newest N of this wave's loads are complete.
+template <int N = 0>
+__device__ __forceinline__ void wait_loads()
+{
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// Swizzle of the 16-byte pieces of a k-contiguous row: with rows of 64 (128,
+// 256) bytes, 16 rows of one piece then lie in 16 different bank groups.
+template <int PR>
+__device__ __forceinline__ int piece_swizzle(int row)
+{
+    return PR == 16 ? row & 15 : PR == 8 ? (row >> 1) & 7 : (row >> 2) & 3;
+}
 
 __device__ __forceinline__ unsigned lds_address(const void* p)
 {
     return (unsigned)(unsigned long long)(lds_void*)p;
 }
 
+// Column-contiguous tiles are [term][BN / 8 pieces]; a transposing read takes 64
+// bytes of each of four consecutive terms.  The 64-byte unit u of term k lies at
+// u ^ unit_swizzle(k), which puts the four into different quarters of the banks
+// (rows of 128 bytes already alternate between two of them).
+template <int BN>
+__device__ __forceinline__ int unit_swizzle(int k)
+{
+    return BN >= 128 ? k & 3 : (k >> 1) & 1;
+}
+
 // Fragments of 16 terms: row pieces of A and columns of B.
 template <class Cfg, int G>
 struct Frags {
-    bf16x8 a[G][Cfg::MT], b[Cfg::NT];
+    bf16x8 a[Cfg::NPL][G][Cfg::MT], b[Cfg::NPL][Cfg::NT];
+};
+
+template <class Cfg, int G>
+struct Acc {
+    f32x16 v[Cfg::NACC][G][Cfg::MT][Cfg::NT];
 };
 
 // aoff and boff are the lane's read offsets, swa its piece swizzle.
 template <class Cfg, int G, bool BTR>
-__device__ __forceinline__ void load_frags(Frags<Cfg, G>& f, const char* sa, const char* sb, int ks, int aoff,
+__device__ __forceinline__ void load_frags(Frags<Cfg, G>& f, const char* stage, int ks, int aoff,
                                            const int (&boff)[Cfg::NT], int h, int swa)
 {
+    const int piece = ((ks * 2 + h) ^ swa) << 4;
 #pragma unroll
-    for (int j = 0; j < Cfg::NT; ++j) {
-        if constexpr (BTR) {
-            typedef __attribute__((address_space(3))) s16x4 lds4;
-            const char* q = sb + boff[j] + ks * (16 * Cfg::BN * 2);
-            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)q);
-            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(q + 4 * Cfg::BN * 2));
-            f.b[j] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-        } else {
-            f.b[j] = *reinterpret_cast<const bf16x8*>(sb + boff[j] + (((ks * 2 + h) ^ swa) << 4));
+    for (int p = 0; p < Cfg::NPL; ++p) {
+        const char *sa = stage + p * Cfg::kA1, *sb = stage + Cfg::NPL * Cfg::kA1 + p * Cfg::kB1;
+#pragma unroll
+        for (int j = 0; j < Cfg::NT; ++j) {
+            if constexpr (BTR) {
+                typedef __attribute__((address_space(3))) s16x4 lds4;
+                const char* q = sb + boff[j] + ks * (16 * Cfg::BN * 2);
+                const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)q);
+                const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(q + 4 * Cfg::BN * 2));
+                f.b[p][j] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+            } else {
+                f.b[p][j] = *reinterpret_cast<const bf16x8*>(sb + boff[j] + piece);
+            }
         }
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int i = 0; i < Cfg::MT; ++i)
+                f.a[p][g][i] = *reinterpret_cast<const bf16x8*>(sa + (g * Cfg::BMG + i * Cfg::WM * 32) * (Cfg::BK * 2) +
+                                                                aoff + piece);
     }
-#pragma unroll
-    for (int g = 0; g < G; ++g)
-#pragma unroll
-        for (int i = 0; i < Cfg::MT; ++i)
-            f.a[g][i] = *reinterpret_cast<const bf16x8*>(sa + g * (Cfg::BMG * 128) + aoff + i * (Cfg::WM * 32 * 128) +
-                                                         (((ks * 2 + h) ^ swa) << 4));
 }
 
 // Columns of B along the accumulator's rows: a lane then holds runs of four
 // consecutive columns of one row of the result.
 template <class Cfg, int G>
-__device__ __forceinline__ void multiply(const Frags<Cfg, G>& f, f32x16 (&acc)[G][Cfg::MT][Cfg::NT])
+__device__ __forceinline__ void multiply(const Frags<Cfg, G>& f, Acc<Cfg, G>& acc)
 {
+    const auto pair = [&](auto pa, auto pb, auto to) {
 #pragma unroll
-    for (int g = 0; g < G; ++g)
+        for (int g = 0; g < G; ++g)
 #pragma unroll
-        for (int i = 0; i < Cfg::MT; ++i)
+            for (int i = 0; i < Cfg::MT; ++i)
 #pragma unroll
-            for (int j = 0; j < Cfg::NT; ++j)
-                acc[g][i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.b[j], f.a[g][i], acc[g][i][j], 0, 0, 0);
+                for (int j = 0; j < Cfg::NT; ++j)
+                    acc.v[to][g][i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.b[pb][j], f.a[pa][g][i],
+                                                                                  acc.v[to][g][i][j], 0, 0, 0);
+    };
+    constexpr std::integral_constant<int, 0> c0{};
+    if constexpr (Cfg::NPL == 3) {
+        constexpr std::integral_constant<int, 1> c1{};
+        constexpr std::integral_constant<int, 2> c2{};
+        pair(c2, c0, c1);
+        pair(c1, c1, c1);
+        pair(c0, c2, c1);
+        pair(c1, c0, c1);
+        pair(c0, c1, c1);
+    }
+    pair(c0, c0, c0);
 }
 
 // Sum over phases [p0, p0 + np) into acc, G row groups.
 template <class Cfg, int G, bool BTR>
 __device__ __forceinline__ void tile_product(const TileArgs& a, int p0, int np, const Mat& ma, const Mat& mb, int K,
-                                             int kb, int ke, int m0, int n0, char* As, char* Bs,
-                                             f32x16 (&acc)[G][Cfg::MT][Cfg::NT])
+                                             int kb, int ke, int m0, int n0, char* S, Acc<Cfg, G>& acc)
 {
-    constexpr int NTH = Cfg::NTH, BN = Cfg::BN, BMG = Cfg::BMG;
-    constexpr int NA = G * BMG * 8 / NTH, NB = Cfg::NB;
+    constexpr int NTH = Cfg::NTH, BN = Cfg::BN, BMG = Cfg::BMG, BK = Cfg::BK, PR = Cfg::PR, NST = Cfg::NST;
+    constexpr int NA = G * BMG * PR / NTH, NB = BN * PR / NTH, RP = NTH / PR;  // pieces a thread, rows a pass
+    constexpr int kPer = Cfg::NPL * (NA + NB);                                // loads a thread and stage
+    static_assert(NA * NTH == G * BMG * PR && NB * NTH == BN * PR && RP % 16 == 0 && BMG % RP == 0);
+    static_assert((NST - 1) * kPer < 64, "vmcnt");
     const int t = (int)threadIdx.x, lane = t & 63;
     const int w = __builtin_amdgcn_readfirstlane(t >> 6), wm = w / Cfg::WN, wn = w % Cfg::WN;
-    const int steps = (ke - kb + kBK - 1) / kBK;
+    const int steps = (ke - kb + BK - 1) / BK;
     if (steps <= 0 || np <= 0) return;
-    // This thread's pieces.  k-contiguous tiles are [row][8 pieces of 8 terms],
-    // piece c of row r in slot c ^ (r / 2 % 8): 16 rows of one piece then cover
-    // all 64 banks.  Column-contiguous tiles are [term][BN / 8 pieces], piece c
-    // of term k in slot c ^ (k % 4 * 4): the four terms of a transposing read
-    // then lie in different 64-byte quarters of the banks.
-    const int ar = t >> 3, ac = ((t & 7) ^ ((t >> 4) & 7)) * 8;
+    // This thread's pieces; k-contiguous tiles are [row][PR pieces of 8 terms].
+    const int ar = t / PR, ac = ((t % PR) ^ piece_swizzle<PR>(ar)) * 8;
     const __bf16 *pa[NA], *pb[NB];
     int la = 0, lb = 0;
-    const auto rows = [&](const __bf16* base, const Mat& m, int row, long long koff) {
-        return base + (long long)row * m.ld + koff;
-    };
     const auto start = [&](int p) {
         const long long k = kb + ac, qa = ma.L > k ? 0 : k / ma.L;
         la = (int)(k - qa * ma.L);
 #pragma unroll
         for (int j = 0; j < NA; ++j) {
-            const int r = j * (NTH / 8) + ar, g = G > 1 && r >= BMG ? 1 : 0;
+            const int r = j * RP + ar, g = G > 1 && r >= BMG ? 1 : 0;
             int row = m0 + (r - g * BMG) + (g ? a.goff : 0);
             row = row < a.M ? row : a.M - 1;  // rows past the end are computed and not stored
-            pa[j] = rows(g ? a.A1[p] : a.A0[p], ma, row, qa * ma.sb + la);
+            pa[j] = (g ? a.A1[p] : a.A0[p]) + (long long)row * ma.ld + qa * ma.sb + la;
         }
         if constexpr (BTR) {
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
-                const int e = j * NTH + t, kk = e / (BN / 8), c = (e % (BN / 8)) ^ ((kk & 3) << 2);
+                const int e = j * NTH + t, kk = e / (BN / 8), c = (e % (BN / 8)) ^ (unit_swizzle<BN>(kk) << 2);
                 int n = n0 + c * 8;
                 n = n < a.N ? n : 0;
                 const int q = n / mb.L;
@@ -185,24 +231,26 @@ __device__ __forceinline__ void tile_product(const TileArgs& a, int p0, int np, 
             lb = (int)(k - q * mb.L);
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
-                int row = n0 + j * (NTH / 8) + ar;
+                int row = n0 + j * RP + ar;
                 row = row < a.N ? row : a.N - 1;
-                pb[j] = rows(a.B[p], mb, row, q * mb.sb + lb);
+                pb[j] = a.B[p] + (long long)row * mb.ld + q * mb.sb + lb;
             }
         }
     };
-    int ip = p0, ik = kb;
-    const unsigned lds0 = lds_address(As) + w * 1024, ldsb = lds_address(Bs) + w * 1024;
-    const auto issue = [&](int buf) {
+    int ip = p0, ik = kb, ib = 0;  // next stage to load: phase, first term, buffer
+    const unsigned lds0 = lds_address(S) + w * 1024;
+    const auto issue = [&] {
         const void* z = g_zeros;
-        const unsigned da = lds0 + buf * Cfg::kAB, db = ldsb + buf * Cfg::kBB;
+        const unsigned d = lds0 + ib * Cfg::kStage;
         const bool oka = ik + ac < K;
 #pragma unroll
         for (int j = 0; j < NA; ++j) {
-            to_lds(oka ? (const void*)pa[j] : z, da + j * (NTH * 16));
-            pa[j] += kBK;
+#pragma unroll
+            for (int p = 0; p < Cfg::NPL; ++p)
+                to_lds(oka ? (const void*)(pa[j] + p * ma.plane) : z, d + p * Cfg::kA1 + j * (NTH * 16));
+            pa[j] += BK;
         }
-        la += kBK;
+        la += BK;
         while (la >= ma.L) {
             la -= ma.L;
 #pragma unroll
@@ -211,65 +259,80 @@ __device__ __forceinline__ void tile_product(const TileArgs& a, int p0, int np, 
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
             const bool ok = BTR ? ik + (j * NTH + t) / (BN / 8) < K : oka;
-            to_lds(ok ? (const void*)pb[j] : z, db + j * (NTH * 16));
-            pb[j] += BTR ? (long long)kBK * mb.ld : (long long)kBK;
+#pragma unroll
+            for (int p = 0; p < Cfg::NPL; ++p)
+                to_lds(ok ? (const void*)(pb[j] + p * mb.plane) : z,
+                       d + Cfg::NPL * Cfg::kA1 + p * Cfg::kB1 + j * (NTH * 16));
+            pb[j] += BTR ? (long long)BK * mb.ld : (long long)BK;
         }
         if constexpr (!BTR) {
-            lb += kBK;
+            lb += BK;
             while (lb >= mb.L) {
                 lb -= mb.L;
 #pragma unroll
                 for (int j = 0; j < NB; ++j) pb[j] += mb.sb - mb.L;
             }
         }
-        ik += kBK;
+        ib = ib + 1 < NST ? ib + 1 : 0;
+        ik += BK;
         if (ik >= ke) {
             ik = kb;
             if (++ip < p0 + np) start(ip);
         }
     };
     // Read addresses.
-    const int h = lane >> 5, swa = (lane >> 1) & 7;
-    const int arow = (wm * 32 + (lane & 31)) * 128;
+    const int h = lane >> 5, swa = piece_swizzle<PR>(lane & 31);
+    const int arow = (wm * 32 + (lane & 31)) * (BK * 2);
     int boff[Cfg::NT];
 #pragma unroll
     for (int j = 0; j < Cfg::NT; ++j) {
         const int nb = (j * Cfg::WN + wn) * 32;
         if constexpr (BTR) {
             const int i = lane & 15, kk = 8 * h + (i >> 2);
-            boff[j] = kk * (BN * 2) + (((nb >> 5) ^ (i >> 2)) << 6) + ((lane >> 4) & 1) * 32 + (i & 3) * 8;
+            boff[j] = kk * (BN * 2) + (((nb >> 5) ^ unit_swizzle<BN>(i >> 2)) << 6) + ((lane >> 4) & 1) * 32 + (i & 3) * 8;
         } else {
-            boff[j] = (nb + (lane & 31)) * 128;
+            boff[j] = (nb + (lane & 31)) * (BK * 2);
         }
     }
-    start(p0);
-    issue(0);
     const int total = steps * np;
-    wait_loads();
+    start(p0);
+    for (int i = 0; i < NST && i < total; ++i) issue();
+    if (total >= NST) wait_loads<(NST - 1) * kPer>();
+    else wait_loads();
     __syncthreads();
-    if (total > 1) issue(1);
     // A step's fragments are read while the step before multiplies.  The barrier
     // that ends a stage comes before its last multiplication: by then every wave
     // has the stage's last fragments in registers, so its buffer can be filled
     // again, and the next stage's first fragments are read behind that work.
-    Frags<Cfg, G> f0, f1;
-    load_frags<Cfg, G, BTR>(f0, As, Bs, 0, arow, boff, h, swa);
+    constexpr int KS = BK / 16;
+    static_assert(KS % 2 == 0);
+    Frags<Cfg, G> f[2];
+    int buf = 0;
+    load_frags<Cfg, G, BTR>(f[0], S, 0, arow, boff, h, swa);
     for (int it = 0; it < total; ++it) {
-        const int buf = it & 1;
-        const char *sa = As + buf * Cfg::kAB, *sb = Bs + buf * Cfg::kBB;
-        load_frags<Cfg, G, BTR>(f1, sa, sb, 1, arow, boff, h, swa);
-        multiply<Cfg, G>(f0, acc);
-        load_frags<Cfg, G, BTR>(f0, sa, sb, 2, arow, boff, h, swa);
-        multiply<Cfg, G>(f1, acc);
-        load_frags<Cfg, G, BTR>(f1, sa, sb, 3, arow, boff, h, swa);
-        multiply<Cfg, G>(f0, acc);
-        if (it + 1 < total) {
-            wait_loads();
-            __syncthreads();
-            if (it + 2 < total) issue(buf);
-            load_frags<Cfg, G, BTR>(f0, As + (buf ^ 1) * Cfg::kAB, Bs + (buf ^ 1) * Cfg::kBB, 0, arow, boff, h, swa);
+        const char* stage = S + buf * Cfg::kStage;
+        buf = buf + 1 < NST ? buf + 1 : 0;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            if (ks + 1 < KS) {
+                load_frags<Cfg, G, BTR>(f[(ks + 1) & 1], stage, ks + 1, arow, boff, h, swa);
+            } else if (it + 1 < total) {
+                if (it + NST <= total) wait_loads<(NST - 2) * kPer>();
+                else wait_loads();
+                __syncthreads();
+                if (it + NST < total) issue();
+                load_frags<Cfg, G, BTR>(f[0], S + buf * Cfg::kStage, 0, arow, boff, h, swa);
+            }
+            multiply<Cfg, G>(f[ks & 1], acc);
         }
-        multiply<Cfg, G>(f1, acc);
+    }
+    if constexpr (Cfg::NPL == 3) {
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int i = 0; i < Cfg::MT; ++i)
+#pragma unroll
+                for (int j = 0; j < Cfg::NT; ++j) acc.v[0][g][i][j] += acc.v[1][g][i][j];
     }
 }
 
@@ -339,6 +402,7 @@ struct Sub {
 // Eight columns of row m into the planes of an intermediate matrix; columns past
 // N are written as zeros up to the row's padding, where the weight gradients
 // read them as terms.
+template <int NPL>
 __device__ __forceinline__ void store_plane(const TileArgs& a, void* o, int m, int n, float (&f)[8])
 {
     if (n >= a.ldo) return;
@@ -347,7 +411,7 @@ __device__ __forceinline__ void store_plane(const TileArgs& a, void* o, int m, i
         for (int i = 0; i < 8; ++i) f[i] = n + i < a.N ? f[i] : 0.0f;
     }
     __bf16* q = (__bf16*)o + (long long)m * a.ldo + n;
-    if (a.npl == 1) {
+    if constexpr (NPL == 1) {
         store_pack<__bf16, 8>(q, f, 8);
         return;
     }
@@ -384,7 +448,7 @@ __device__ __forceinline__ void store_out(const TileArgs& a, void* o, int m, int
 template <class Cfg, int EPI>
 constexpr int tile_lds()
 {
-    const int stages = 2 * (Cfg::kAB + Cfg::kBB), out = (EPI == kEpiGrad ? 3 : 2) * Sub<Cfg>::kBytes;
+    const int stages = Cfg::NST * Cfg::kStage, out = (EPI == kEpiGrad ? 3 : 2) * Sub<Cfg>::kBytes;
     return stages > out ? stages : out;
 }
 
@@ -392,7 +456,6 @@ template <class Cfg, bool BTR, int EPI>
 __global__ __launch_bounds__(Cfg::NTH) void k_ffn_tile(TileArgs a)
 {
     __shared__ __align__(1024) char S[tile_lds<Cfg, EPI>()];
-    char *As = S, *Bs = S + 2 * Cfg::kAB;
     // Workgroups are dealt to the eight XCDs in turn: each takes a contiguous run
     // of tiles, in columns of up to kTileRows row tiles, so that the operands
     // its workgroups share stay in its own L2.
@@ -403,12 +466,12 @@ __global__ __launch_bounds__(Cfg::NTH) void k_ffn_tile(TileArgs a)
     const int left = a.tm - band * kTileRows, bm = left < kTileRows ? left : kTileRows;
     const int m0 = (band * kTileRows + in % bm) * (a.goff ? 2 * Cfg::BMG : Cfg::BMG), n0 = (in / bm) * Cfg::BN;
     const int kb = s * a.kper, ke = kb + a.kper < a.K ? kb + a.kper : a.K;
-    f32x16 acc[2][Cfg::MT][Cfg::NT] = {};
-    tile_product<Cfg, 2, BTR>(a, 0, a.n1, a.ma, a.mb, a.K, kb, ke, m0, n0, As, Bs, acc);
-    f32x16 dh[1][Cfg::MT][Cfg::NT] = {};
+    Acc<Cfg, 2> acc{};
+    tile_product<Cfg, 2, BTR>(a, 0, a.n1, a.ma, a.mb, a.K, kb, ke, m0, n0, S, acc);
+    Acc<Cfg, 1> dh{};
     if constexpr (EPI == kEpiGrad) {
         __syncthreads();
-        tile_product<Cfg, 1, BTR>(a, a.n1, a.n2, a.ma2, a.mb2, a.K2, 0, a.K2, m0, n0, As, Bs, dh);
+        tile_product<Cfg, 1, BTR>(a, a.n1, 1, a.ma2, a.mb2, a.K2, 0, a.K2, m0, n0, S, dh);
     }
     typedef Sub<Cfg> E;
     char *S0 = S, *S1 = S + E::kBytes, *S2 = S + 2 * E::kBytes;
@@ -417,9 +480,9 @@ __global__ __launch_bounds__(Cfg::NTH) void k_ffn_tile(TileArgs a)
 #pragma unroll
         for (int j = 0; j < Cfg::NT; ++j) {
             __syncthreads();
-            E::put(S0, acc[0][i][j]);
-            E::put(S1, acc[1][i][j]);
-            if constexpr (EPI == kEpiGrad) E::put(S2, dh[0][i][j]);
+            E::put(S0, acc.v[0][0][i][j]);
+            E::put(S1, acc.v[0][1][i][j]);
+            if constexpr (EPI == kEpiGrad) E::put(S2, dh.v[0][0][i][j]);
             __syncthreads();
             E::pieces([&](int row, int col) {
                 const int m = m0 + i * E::SR + row, n = n0 + j * E::SC + col;
@@ -449,7 +512,7 @@ __global__ __launch_bounds__(Cfg::NTH) void k_ffn_tile(TileArgs a)
 #pragma unroll
                             for (int r = 0; r < 8; ++r) f0[r] = act_fwd(act, f0[r]) * f1[r];
                         });
-                        store_plane(a, a.o0, m, n, f0);
+                        store_plane<Cfg::NPL>(a, a.o0, m, n, f0);
                     } else {
                         float d[8], du[8];
                         E::get(S2, row, col, d);
@@ -463,9 +526,9 @@ __global__ __launch_bounds__(Cfg::NTH) void k_ffn_tile(TileArgs a)
                                 f1[r] = d[r] * f1[r] * da;
                             }
                         });
-                        store_plane(a, a.o0, m, n, f0);
-                        store_plane(a, a.o1, m, n, f1);
-                        store_plane(a, a.o2, m, n, du);
+                        store_plane<Cfg::NPL>(a, a.o0, m, n, f0);
+                        store_plane<Cfg::NPL>(a, a.o1, m, n, f1);
+                        store_plane<Cfg::NPL>(a, a.o2, m, n, du);
                     }
                 }
             });

@@ -88,9 +88,46 @@ __global__ __launch_bounds__(256) void k_ffn_zero(unsigned short* p, long long n
     if (i < n) p[i] = 0;
 }
 
-typedef TileCfg<2, 4, 2, 2> Big;  // 128 (x 2 groups) x 256, 512 threads, one workgroup per CU
-typedef TileCfg<2, 2, 1, 2> Mid;  // 64 (x 2 groups) x 128, 256 threads, two workgroups per CU
+// Tiles.  bf16: Big fills a CU (128 KB of stages, eight waves); Mid runs two
+// workgroups a CU where Big has too few tiles; Small adds stages in flight for
+// launches that cannot fill the device.  fp32 (three planes): Wide and Slim.
+typedef TileCfg<2, 4, 2, 2, 64, 2, 1> Big;    // 128 (x 2 groups) x 256
+typedef TileCfg<2, 2, 1, 2, 64, 2, 1> Mid;    // 64 (x 2) x 128
+typedef TileCfg<2, 2, 1, 1, 64, 4, 1> Small;  // 64 (x 2) x 64
+typedef TileCfg<2, 2, 1, 2, 32, 3, 3> Wide;   // 64 (x 2) x 128
+typedef TileCfg<2, 2, 1, 1, 32, 4, 3> Slim;   // 64 (x 2) x 64
+enum Tile { kBig, kMid, kSmall, kWide, kSlim };
 constexpr int kCUs = 256;
+
+struct TileSize {
+    int bmg, bn, slots;
+};
+
+TileSize tile_size(Tile t)
+{
+    switch (t) {
+    case kBig: return {Big::BMG, Big::BN, kCUs};
+    case kMid: return {Mid::BMG, Mid::BN, 2 * kCUs};
+    case kSmall: return {Small::BMG, Small::BN, kCUs};
+    case kWide: return {Wide::BMG, Wide::BN, kCUs};
+    default: return {Slim::BMG, Slim::BN, kCUs};
+    }
+}
+
+long long tiles_of(Tile t, long long rows, long long cols, bool dual)
+{
+    const TileSize s = tile_size(t);
+    const long long m = s.bmg * (dual ? 1 : 2);
+    return ((rows + m - 1) / m) * ((cols + s.bn - 1) / s.bn);
+}
+
+// The largest tile that still gives (most of) the device's CUs one.
+Tile pick_tile(bool bf16, long long rows, long long cols, bool dual)
+{
+    if (!bf16) return tiles_of(kWide, rows, cols, dual) >= kCUs * 3 / 4 ? kWide : kSlim;
+    if (tiles_of(kBig, rows, cols, dual) >= kCUs * 3 / 4) return kBig;
+    return tiles_of(kMid, rows, cols, dual) >= kCUs * 3 / 4 ? kMid : kSmall;
+}
 
 long long round8(long long v) { return (v + 7) & ~7ll; }
 
@@ -114,7 +151,7 @@ struct Planes {
 // sums' traffic (time in units of one stage of the big tile, about a microsecond).
 int pieces(long long tiles, int slots, long long K, long long elems)
 {
-    const long long steps = (K + kBK - 1) / kBK;
+    const long long steps = (K + kPiece - 1) / kPiece;
     double best = 0.0;
     int pick = 1;
     for (int s = 1; s <= 128 && s <= steps; ++s) {
@@ -125,25 +162,15 @@ int pieces(long long tiles, int slots, long long K, long long elems)
     return pick;
 }
 
-bool use_big(long long rows, long long cols, int groups_rows)
-{
-    return ((rows + groups_rows - 1) / groups_rows) * ((cols + Big::BN - 1) / Big::BN) >= kCUs * 3 / 4;
-}
-
 struct Cut {
-    bool big;
+    Tile tile;
     int splits;
 };
 
-Cut cut_dw(long long rows, long long cols, long long K, bool dual)
+Cut cut_dw(bool bf16, long long rows, long long cols, long long K, bool dual)
 {
-    const long long t_big = ((rows + (dual ? 1 : 2) * Big::BMG - 1) / ((dual ? 1 : 2) * Big::BMG)) *
-                            ((cols + Big::BN - 1) / Big::BN);
-    const long long t_mid = ((rows + (dual ? 1 : 2) * Mid::BMG - 1) / ((dual ? 1 : 2) * Mid::BMG)) *
-                            ((cols + Mid::BN - 1) / Mid::BN);
-    const long long elems = rows * cols * (dual ? 2 : 1);
-    const bool big = rows >= Big::BMG && cols >= Big::BN;
-    return Cut{big, big ? pieces(t_big, kCUs, K, elems) : pieces(t_mid, 2 * kCUs, K, elems)};
+    const Tile t = !bf16 ? kWide : rows >= Big::BMG && cols >= Big::BN ? kBig : kMid;
+    return Cut{t, pieces(tiles_of(t, rows, cols, dual), tile_size(t).slots, K, rows * cols * (dual ? 2 : 1))};
 }
 
 struct Layout {
@@ -182,7 +209,7 @@ Layout layout(int B, int C, int F, long long L, bool bf16, bool bwd)
         take(o.wgt, C, o.Fp);
         take(o.wut, C, o.Fp);
         take(o.wdt, F, o.Cp);
-        const Cut c1 = cut_dw(F, C, o.T, true), c2 = cut_dw(C, F, o.T, false);
+        const Cut c1 = cut_dw(bf16, F, C, o.T, true), c2 = cut_dw(bf16, C, F, o.T, false);
         const size_t e1 = c1.splits > 1 ? (size_t)c1.splits * 2u : 0u, e2 = c2.splits > 1 ? (size_t)c2.splits : 0u;
         o.part = at;
         at += (e1 > e2 ? e1 : e2) * (size_t)F * (size_t)C * 4u;
@@ -205,22 +232,27 @@ hipError_t run_tiles(TileArgs& a, hipStream_t st)
 }
 
 template <bool BTR, int EPI>
-hipError_t run_any(TileArgs& a, bool big, hipStream_t st)
+hipError_t run_any(TileArgs& a, Tile t, hipStream_t st)
 {
-    return big ? run_tiles<Big, BTR, EPI>(a, st) : run_tiles<Mid, BTR, EPI>(a, st);
+    switch (t) {
+    case kBig: return run_tiles<Big, BTR, EPI>(a, st);
+    case kMid: return run_tiles<Mid, BTR, EPI>(a, st);
+    case kSmall:
+        if constexpr (EPI != kEpiPart) return run_tiles<Small, BTR, EPI>(a, st);
+        return hipErrorInvalidValue;
+    case kWide: return run_tiles<Wide, BTR, EPI>(a, st);
+    case kSlim:
+        if constexpr (EPI != kEpiPart) return run_tiles<Slim, BTR, EPI>(a, st);
+        return hipErrorInvalidValue;
+    }
+    return hipErrorInvalidValue;
 }
 
-// The phases of one product: pairs of planes, smallest first.
-int add_phases(TileArgs& a, int at, int npl, const __bf16* A0, const __bf16* A1, long long pa, const __bf16* B,
-               long long pb)
+void set_phase(TileArgs& a, int i, const Planes& A0, const Planes& A1, const Planes& B)
 {
-    static const int ia[6] = {2, 1, 0, 1, 0, 0}, ib[6] = {0, 1, 2, 0, 1, 0};
-    for (int i = npl == 1 ? 5 : 0; i < 6; ++i, ++at) {
-        a.A0[at] = A0 + ia[i] * pa;
-        a.A1[at] = A1 + ia[i] * pa;
-        a.B[at] = B + ib[i] * pb;
-    }
-    return at;
+    a.A0[i] = A0.p;
+    a.A1[i] = A1.p;
+    a.B[i] = B.p;
 }
 
 struct Chain {
@@ -253,11 +285,11 @@ struct Chain {
     {
         if (o.xdirect) {
             *p = Planes{(__bf16*)x, f.L, 0};
-            *m = Mat{f.L, f.C * f.L, (int)f.L};
+            *m = Mat{f.L, f.C * f.L, 0, (int)f.L};
             return hipSuccess;
         }
         *p = planes(off, f.C, o.Tp);
-        *m = Mat{o.Tp, 0, INT_MAX};
+        *m = Mat{o.Tp, 0, p->plane, INT_MAX};
         // One position per batch entry: rows of channels, read along them.
         const View v = f.L == 1 ? View{x, 1, f.C, kFar, 0} : View{x, f.L, 1, f.L, f.C * f.L};
         return pack(v, f.C, (int)o.T, *p, f.L == 1);
@@ -266,12 +298,9 @@ struct Chain {
     hipError_t weight(const void* w, size_t off, int rows, int cols, Planes* p, Mat* m) const
     {
         const long long ld = o.wdirect ? cols : round8(cols);
-        *m = Mat{ld, 0, INT_MAX};
-        if (o.wdirect) {
-            *p = Planes{(__bf16*)w, ld, 0};
-            return hipSuccess;
-        }
-        *p = planes(off, rows, ld);
+        *p = o.wdirect ? Planes{(__bf16*)w, ld, 0} : planes(off, rows, ld);
+        *m = Mat{ld, 0, p->plane, INT_MAX};
+        if (o.wdirect) return hipSuccess;
         return pack(View{w, cols, 1, kFar, 0}, rows, cols, *p, false);
     }
 
@@ -279,8 +308,8 @@ struct Chain {
     hipError_t weight_t(const void* w, size_t off, int rows, int cols, Planes* p, Mat* m) const
     {
         const long long ld = round8(cols);
-        *m = Mat{ld, 0, INT_MAX};
         *p = planes(off, rows, ld);
+        *m = Mat{ld, 0, p->plane, INT_MAX};
         return pack(View{w, 1, rows, kFar, 0}, rows, cols, *p, true);
     }
 
@@ -292,7 +321,6 @@ struct Chain {
         a.K = a.kper = K;
         a.splits = 1;
         a.act = f.act;
-        a.npl = o.npl;
         a.out32 = !f.bf16;
         a.oL = INT_MAX;
         return a;
@@ -321,32 +349,34 @@ struct Chain {
             return launch_ffn_fused(FusedFfn{x.p, wg.p, wu.p, wd.p, f.y, mx.ld, mx.sb, mx.L, mw.ld, md.ld, f.C, f.F,
                                              (int)o.T, f.act, f.L, f.C * f.L, (int)f.L}, st);
         TileArgs a = base(f.F, o.T, f.C);
-        a.n1 = add_phases(a, 0, o.npl, wg.p, wu.p, wg.plane, x.p, x.plane);
+        a.n1 = 1;
+        set_phase(a, 0, wg, wu, x);
         a.ma = mw;
         a.mb = mx;
         a.o0 = h.p;
         a.ldo = o.Tp;
         a.plane = h.plane;
-        if ((e = run_any<true, kEpiGate>(a, use_big(f.F, o.T, Big::BMG), st)) != hipSuccess) return e;
+        if ((e = run_any<true, kEpiGate>(a, pick_tile(f.bf16, f.F, o.T, true), st)) != hipSuccess) return e;
         TileArgs d = base(f.C, o.T, f.F);
-        d.n1 = add_phases(d, 0, o.npl, wd.p, wd.p, wd.plane, h.p, h.plane);
+        d.n1 = 1;
+        set_phase(d, 0, wd, wd, h);
         d.ma = md;
-        d.mb = Mat{o.Tp, 0, INT_MAX};
+        d.mb = Mat{o.Tp, 0, h.plane, INT_MAX};
         to_grid(d, f.y);
-        return run_any<true, kEpiOut>(d, use_big(f.C, o.T, 2 * Big::BMG), st);
+        return run_any<true, kEpiOut>(d, pick_tile(f.bf16, f.C, o.T, false), st);
     }
 
     hipError_t weight_grad(TileArgs& a, bool dual, void* o0, void* o1) const
     {
-        const Cut c = cut_dw(a.M, a.N, o.T, dual);
+        const Cut c = cut_dw(f.bf16, a.M, a.N, o.T, dual);
         a.splits = c.splits;
-        a.kper = (int)(((o.T + kBK - 1) / kBK + c.splits - 1) / c.splits) * kBK;
+        a.kper = (int)(((o.T + kPiece - 1) / kPiece + c.splits - 1) / c.splits) * kPiece;
         a.goff = dual ? 0 : 1;
         a.o0 = o0;
         a.o1 = o1;
         a.o2 = ws + o.part;
         a.ldo = a.N;
-        hipError_t e = run_any<false, kEpiPart>(a, c.big, st);
+        hipError_t e = run_any<false, kEpiPart>(a, c.tile, st);
         if (e != hipSuccess || c.splits == 1) return e;
         const long long n0 = (long long)a.M * a.N, n = n0 * (dual ? 2 : 1);
         const unsigned grid = (unsigned)((n + 255) / 256);
@@ -364,7 +394,7 @@ struct Chain {
         Planes x, dy, wg, wu, wgt, wut, wdt;
         const Planes h = planes(o.h, f.F, o.Tp), dg = planes(o.dg, f.F, o.Tp), du = planes(o.du, f.F, o.Tp);
         Mat mx, mw, mt, mdt;
-        const Mat mh{o.Tp, 0, INT_MAX};
+        const Mat mh{o.Tp, 0, h.plane, INT_MAX};
         hipError_t e;
         if ((e = act(f.x, o.x, &x, &mx)) != hipSuccess || (e = act(f.dy, o.dy, &dy, &mx)) != hipSuccess ||
             (e = weight(f.Wg, o.wg, f.F, f.C, &wg, &mw)) != hipSuccess ||
@@ -375,8 +405,9 @@ struct Chain {
             return e;
         // h, dg, du
         TileArgs a = base(f.F, o.T, f.C);
-        a.n1 = add_phases(a, 0, o.npl, wg.p, wu.p, wg.plane, x.p, x.plane);
-        a.n2 = add_phases(a, a.n1, o.npl, wdt.p, wdt.p, wdt.plane, dy.p, dy.plane) - a.n1;
+        a.n1 = 1;
+        set_phase(a, 0, wg, wu, x);
+        set_phase(a, 1, wdt, wdt, dy);
         a.ma = mw;
         a.mb = a.mb2 = mx;
         a.ma2 = mdt;
@@ -386,24 +417,27 @@ struct Chain {
         a.o2 = du.p;
         a.ldo = o.Tp;
         a.plane = h.plane;
-        if ((e = run_any<true, kEpiGrad>(a, use_big(f.F, o.T, Big::BMG), st)) != hipSuccess) return e;
+        if ((e = run_any<true, kEpiGrad>(a, pick_tile(f.bf16, f.F, o.T, true), st)) != hipSuccess) return e;
         // dx
         TileArgs d = base(f.C, o.T, f.F);
-        const int half = add_phases(d, 0, o.npl, wgt.p, wgt.p, wgt.plane, dg.p, dg.plane);
-        d.n1 = add_phases(d, half, o.npl, wut.p, wut.p, wut.plane, du.p, du.plane);
+        d.n1 = 2;
+        set_phase(d, 0, wgt, wgt, dg);
+        set_phase(d, 1, wut, wut, du);
         d.ma = mt;
         d.mb = mh;
         to_grid(d, f.dx);
-        if ((e = run_any<true, kEpiOut>(d, use_big(f.C, o.T, 2 * Big::BMG), st)) != hipSuccess) return e;
+        if ((e = run_any<true, kEpiOut>(d, pick_tile(f.bf16, f.C, o.T, false), st)) != hipSuccess) return e;
         // dWg, dWu
         TileArgs w = base(f.F, f.C, (int)o.T);
-        w.n1 = add_phases(w, 0, o.npl, dg.p, du.p, dg.plane, x.p, x.plane);
+        w.n1 = 1;
+        set_phase(w, 0, dg, du, x);
         w.ma = mh;
         w.mb = mx;
         if ((e = weight_grad(w, true, f.dWg, f.dWu)) != hipSuccess) return e;
         // dWd
         TileArgs v = base(f.C, f.F, (int)o.T);
-        v.n1 = add_phases(v, 0, o.npl, dy.p, dy.p, dy.plane, h.p, h.plane);
+        v.n1 = 1;
+        set_phase(v, 0, dy, dy, h);
         v.ma = mx;
         v.mb = mh;
         return weight_grad(v, false, f.dWd, nullptr);

@@ -48,14 +48,6 @@ struct FusedCfg {
     static constexpr int kBytes = 2 * kStage + kX > kOut ? 2 * kStage + kX : kOut;
 };
 
-// Swizzle of a weight row's pieces: rows of 64, 128 and 256 bytes put 16 rows
-// of one piece into 16 different bank groups.
-template <int PR>
-__device__ __forceinline__ int piece_swizzle(int row)
-{
-    return PR == 16 ? row & 15 : PR == 8 ? (row >> 1) & 7 : (row >> 2) & 3;
-}
-
 template <int KC>
 __global__ __launch_bounds__(256, 2) void k_ffn_fused(FusedArgs a)
 {
@@ -262,7 +254,7 @@ hipError_t launch_ffn_fused(const FusedFfn& f, hipStream_t st)
     a.wu = (const __bf16*)f.wu;
     a.wd = (const __bf16*)f.wd;
     a.y = f.y;
-    a.mx = Mat{f.ldx, f.sbx, f.Lx};
+    a.mx = Mat{f.ldx, f.sbx, 0, f.Lx};
     a.ldw = f.ldw;
     a.ldd = f.ldd;
     a.C = f.C;
