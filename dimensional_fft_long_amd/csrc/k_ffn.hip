@@ -28,14 +28,32 @@ struct View {
     long long sr, st, L, sb;
 };
 
+// One operand to bring into planes; a launch does all of a chain's.
+struct PackJob {
+    View v;
+    __bf16* dst;
+    long long plane;
+    int rows, cols, ld;
+    bool by_row;          // threads along the rows (the direction contiguous in the source)
+    unsigned first;       // first workgroup
+};
+constexpr int kMaxJobs = 7;
+struct PackJobs {
+    PackJob j[kMaxJobs];
+    int n;
+};
+
 template <class T, int NPL>
-__global__ __launch_bounds__(256) void k_ffn_pack(View v, int rows, int cols, int ld, __bf16* dst, long long plane,
-                                                  bool by_row)
+__global__ __launch_bounds__(256) void k_ffn_pack(PackJobs jobs)
 {
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    int which = 0;
+    while (which + 1 < jobs.n && blockIdx.x >= jobs.j[which + 1].first) ++which;
+    const PackJob& job = jobs.j[which];
+    const View& v = job.v;
+    const int rows = job.rows, cols = job.cols, ld = job.ld;
+    const long long i = (long long)(blockIdx.x - job.first) * 256 + threadIdx.x;
     const int gc = ld / 8;
-    // Threads along the direction that is contiguous in the source.
-    const long long r = by_row ? i % rows : i / gc, g = by_row ? i / rows : i % gc;
+    const long long r = job.by_row ? i % rows : i / gc, g = job.by_row ? i / rows : i % gc;
     if (r >= rows || g >= gc) return;
     const long long t0 = g * 8;
     float f[8];
@@ -52,7 +70,7 @@ __global__ __launch_bounds__(256) void k_ffn_pack(View v, int rows, int cols, in
             f[j] = t < cols ? (float)s[qq * v.sb + (t - qq * v.L) * v.st] : 0.0f;
         }
     }
-    __bf16* d = dst + r * ld + t0;
+    __bf16* d = job.dst + r * ld + t0;
     if constexpr (NPL == 1) {
         store_pack<__bf16, 8>(d, f, 8);
     } else {
@@ -65,7 +83,7 @@ __global__ __launch_bounds__(256) void k_ffn_pack(View v, int rows, int cols, in
             for (int k = 0; k < 3; ++k) s3[k][j] = p[k];
         }
 #pragma unroll
-        for (int k = 0; k < 3; ++k) store_pack<__bf16, 8>(d + k * plane, s3[k], 8);
+        for (int k = 0; k < 3; ++k) store_pack<__bf16, 8>(d + k * job.plane, s3[k], 8);
     }
 }
 
@@ -77,6 +95,7 @@ __global__ __launch_bounds__(256) void k_ffn_sum(const float* part, int splits, 
     const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
     if (i >= n) return;
     float s = 0.0f;
+#pragma unroll 8
     for (int p = 0; p < splits; ++p) s += part[(long long)p * n + i];
     if (i < n0) o0[i] = (T)s;
     else o1[i - n0] = (T)s;
@@ -260,6 +279,8 @@ struct Chain {
     Layout o;
     hipStream_t st;
     char* ws;
+    PackJobs jobs{};
+    unsigned blocks = 0;
 
     Chain(const FfnArgs& a, bool bwd, hipStream_t s)
         : f(a), o(layout(a.B, a.C, a.F, a.L, a.bf16, bwd)), st(s), ws((char*)a.ws)
@@ -267,50 +288,52 @@ struct Chain {
     }
     Planes planes(size_t off, long long rows, long long ld) const { return {(__bf16*)(ws + off), ld, rows * ld}; }
 
-    hipError_t pack(const View& v, int rows, int cols, const Planes& d, bool by_row) const
+    void pack(const View& v, int rows, int cols, const Planes& d, bool by_row)
     {
-        const long long n = rows * (d.ld / 8);
-        const unsigned grid = (unsigned)((n + 255) / 256);
-        if (f.bf16)
-            hipLaunchKernelGGL((k_ffn_pack<__bf16, 1>), dim3(grid), dim3(256), 0, st, v, rows, cols, (int)d.ld, d.p,
-                               d.plane, by_row);
-        else
-            hipLaunchKernelGGL((k_ffn_pack<float, 3>), dim3(grid), dim3(256), 0, st, v, rows, cols, (int)d.ld, d.p,
-                               d.plane, by_row);
+        PackJob& j = jobs.j[jobs.n++];
+        j = PackJob{v, d.p, d.plane, rows, cols, (int)d.ld, by_row, blocks};
+        blocks += (unsigned)((rows * (d.ld / 8) + 255) / 256);
+    }
+
+    // The passes asked for so far, in one launch.
+    hipError_t run_packs() const
+    {
+        if (jobs.n == 0) return hipSuccess;
+        if (f.bf16) hipLaunchKernelGGL((k_ffn_pack<__bf16, 1>), dim3(blocks), dim3(256), 0, st, jobs);
+        else hipLaunchKernelGGL((k_ffn_pack<float, 3>), dim3(blocks), dim3(256), 0, st, jobs);
         return launch_status();
     }
 
     // Activations [B][C][L] as an operand: where they lie, or packed at off.
-    hipError_t act(const void* x, size_t off, Planes* p, Mat* m) const
+    void act(const void* x, size_t off, Planes* p, Mat* m)
     {
         if (o.xdirect) {
             *p = Planes{(__bf16*)x, f.L, 0};
             *m = Mat{f.L, f.C * f.L, 0, (int)f.L};
-            return hipSuccess;
+            return;
         }
         *p = planes(off, f.C, o.Tp);
         *m = Mat{o.Tp, 0, p->plane, INT_MAX};
         // One position per batch entry: rows of channels, read along them.
         const View v = f.L == 1 ? View{x, 1, f.C, kFar, 0} : View{x, f.L, 1, f.L, f.C * f.L};
-        return pack(v, f.C, (int)o.T, *p, f.L == 1);
+        pack(v, f.C, (int)o.T, *p, f.L == 1);
     }
 
-    hipError_t weight(const void* w, size_t off, int rows, int cols, Planes* p, Mat* m) const
+    void weight(const void* w, size_t off, int rows, int cols, Planes* p, Mat* m)
     {
         const long long ld = o.wdirect ? cols : round8(cols);
         *p = o.wdirect ? Planes{(__bf16*)w, ld, 0} : planes(off, rows, ld);
         *m = Mat{ld, 0, p->plane, INT_MAX};
-        if (o.wdirect) return hipSuccess;
-        return pack(View{w, cols, 1, kFar, 0}, rows, cols, *p, false);
+        if (!o.wdirect) pack(View{w, cols, 1, kFar, 0}, rows, cols, *p, false);
     }
 
     // w [cols][rows] transposed.
-    hipError_t weight_t(const void* w, size_t off, int rows, int cols, Planes* p, Mat* m) const
+    void weight_t(const void* w, size_t off, int rows, int cols, Planes* p, Mat* m)
     {
         const long long ld = round8(cols);
         *p = planes(off, rows, ld);
         *m = Mat{ld, 0, p->plane, INT_MAX};
-        return pack(View{w, 1, rows, kFar, 0}, rows, cols, *p, true);
+        pack(View{w, 1, rows, kFar, 0}, rows, cols, *p, true);
     }
 
     TileArgs base(int M, long long N, int K) const
@@ -336,15 +359,16 @@ struct Chain {
         a.goff = 1;
     }
 
-    hipError_t forward() const
+    hipError_t forward()
     {
         Planes x, wg, wu, wd, h = planes(o.h, f.F, o.Tp);
         Mat mx, mw, md;
         hipError_t e;
-        if ((e = act(f.x, o.x, &x, &mx)) != hipSuccess || (e = weight(f.Wg, o.wg, f.F, f.C, &wg, &mw)) != hipSuccess ||
-            (e = weight(f.Wu, o.wu, f.F, f.C, &wu, &mw)) != hipSuccess ||
-            (e = weight(f.Wd, o.wd, f.C, f.F, &wd, &md)) != hipSuccess)
-            return e;
+        act(f.x, o.x, &x, &mx);
+        weight(f.Wg, o.wg, f.F, f.C, &wg, &mw);
+        weight(f.Wu, o.wu, f.F, f.C, &wu, &mw);
+        weight(f.Wd, o.wd, f.C, f.F, &wd, &md);
+        if ((e = run_packs()) != hipSuccess) return e;
         if (f.bf16 && f.C <= kFusedMaxC)
             return launch_ffn_fused(FusedFfn{x.p, wg.p, wu.p, wd.p, f.y, mx.ld, mx.sb, mx.L, mw.ld, md.ld, f.C, f.F,
                                              (int)o.T, f.act, f.L, f.C * f.L, (int)f.L}, st);
@@ -389,20 +413,21 @@ struct Chain {
         return launch_status();
     }
 
-    hipError_t backward() const
+    hipError_t backward()
     {
         Planes x, dy, wg, wu, wgt, wut, wdt;
         const Planes h = planes(o.h, f.F, o.Tp), dg = planes(o.dg, f.F, o.Tp), du = planes(o.du, f.F, o.Tp);
         Mat mx, mw, mt, mdt;
         const Mat mh{o.Tp, 0, h.plane, INT_MAX};
         hipError_t e;
-        if ((e = act(f.x, o.x, &x, &mx)) != hipSuccess || (e = act(f.dy, o.dy, &dy, &mx)) != hipSuccess ||
-            (e = weight(f.Wg, o.wg, f.F, f.C, &wg, &mw)) != hipSuccess ||
-            (e = weight(f.Wu, o.wu, f.F, f.C, &wu, &mw)) != hipSuccess ||
-            (e = weight_t(f.Wg, o.wgt, f.C, f.F, &wgt, &mt)) != hipSuccess ||
-            (e = weight_t(f.Wu, o.wut, f.C, f.F, &wut, &mt)) != hipSuccess ||
-            (e = weight_t(f.Wd, o.wdt, f.F, f.C, &wdt, &mdt)) != hipSuccess)
-            return e;
+        act(f.x, o.x, &x, &mx);
+        act(f.dy, o.dy, &dy, &mx);
+        weight(f.Wg, o.wg, f.F, f.C, &wg, &mw);
+        weight(f.Wu, o.wu, f.F, f.C, &wu, &mw);
+        weight_t(f.Wg, o.wgt, f.C, f.F, &wgt, &mt);
+        weight_t(f.Wu, o.wut, f.C, f.F, &wut, &mt);
+        weight_t(f.Wd, o.wdt, f.F, f.C, &wdt, &mdt);
+        if ((e = run_packs()) != hipSuccess) return e;
         // h, dg, du
         TileArgs a = base(f.F, o.T, f.C);
         a.n1 = 1;
