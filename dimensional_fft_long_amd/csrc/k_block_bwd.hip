@@ -53,7 +53,8 @@ __global__ __launch_bounds__(NT, NT == 1024 ? 4 : V * K <= (JOIN ? 8 : 16) ? 4 :
 #pragma unroll
         for (int v = 0; v < VA; ++v) Q[k][v] = S[k][v] = 0.0f;
     Where<V, ROW> w(a, g);
-    for (long long tile = blockIdx.x; tile < g.tiles; tile += gridDim.x) {
+    const Run tiles(g);
+    for (long long tile = tiles.first; tile < tiles.end; tile += tiles.step) {
         w.at(a, g, tile);
         Pack<T, V> xr[K], mr[JOIN ? K : 1], gr[JOIN ? K : 1], hr[K], dr[K];
 #pragma unroll

@@ -42,7 +42,8 @@ __global__ __launch_bounds__(kNT, V * K <= 32 ? 4 : 2) void k_block_fwd(BlockArg
         wpre.load(a.w_pre, w, 0.0f);
     }
     Where<V, ROW> w(a, g);
-    for (long long tile = blockIdx.x; tile < g.tiles; tile += gridDim.x) {
+    const Run tiles(g);
+    for (long long tile = tiles.first; tile < tiles.end; tile += tiles.step) {
         w.at(a, g, tile);
         Pack<T, V> xr[K], mr[JOIN ? K : 1], gr[JOIN ? K : 1];
 #pragma unroll
