@@ -52,19 +52,33 @@ __global__ __launch_bounds__(NT, NT == 1024 ? 4 : V * K <= (JOIN ? 8 : 16) ? 4 :
     for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int v = 0; v < VA; ++v) Q[k][v] = S[k][v] = 0.0f;
-    Where<V, ROW> w(a, g);
-    const Run tiles(g);
-    for (long long tile = tiles.first; tile < tiles.end; tile += tiles.step) {
-        w.at(a, g, tile);
-        Pack<T, V> xr[K], mr[JOIN ? K : 1], gr[JOIN ? K : 1], hr[K], dr[K];
+    Pack<T, V> xr[K], mr[JOIN ? K : 1], gr[JOIN ? K : 1], hr[K], dr[K];
+    const auto load = [&](const Where<V, ROW>& at) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            if (JOIN) mr[k] = load_group<T, V, ROW>(a.m, w, k);
+            if (JOIN) mr[k] = load_group<T, V, ROW>(a.m, at, k);
             if (a.dh) {
-                xr[k] = load_group<T, V, ROW>(a.x, w, k);
-                hr[k] = load_group<T, V, ROW>(a.dh, w, k);
+                xr[k] = load_group<T, V, ROW>(a.x, at, k);
+                hr[k] = load_group<T, V, ROW>(a.dh, at, k);
             }
-            if (JOIN && a.gate) gr[k] = load_group<T, V, ROW>(a.gate, w, k);
+            if (JOIN && a.gate) gr[k] = load_group<T, V, ROW>(a.gate, at, k);
+        }
+    };
+    // The norm asks for the next tile's tensors ahead of this tile's stores (89 ->
+    // 81 us at 2 x 1024 x 16384 bf16; nothing gained for the join's five tensors).
+    constexpr bool AHEAD = !JOIN;
+    const Run tiles(g);
+    Where<V, ROW> w(a, g), wn(a, g);
+    if (AHEAD && tiles.first < tiles.end) {
+        w.at(a, g, tiles.first);
+        load(w);
+    }
+    for (long long tile = tiles.first; tile < tiles.end; tile += tiles.step) {
+        const bool more = AHEAD && tile + tiles.step < tiles.end;
+        if (more) wn.at(a, g, tile + tiles.step);
+        if (!AHEAD) {
+            w.at(a, g, tile);
+            load(w);
         }
         // Dropout's words while the loads are in flight.
         unsigned keep[JOIN ? K : 1];
@@ -166,6 +180,7 @@ __global__ __launch_bounds__(NT, NT == 1024 ? 4 : V * K <= (JOIN ? 8 : 16) ? 4 :
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
+            if (more) load(wn);
             if constexpr (JOIN) {
                 if (a.w_post) {
                     sum_channels<1, V, ROW, NT>(em, red, turn, g.lxs);
@@ -182,6 +197,7 @@ __global__ __launch_bounds__(NT, NT == 1024 ? 4 : V * K <= (JOIN ? 8 : 16) ? 4 :
                 }
             }
         });
+        if (AHEAD) w = wn;
     }
     // Partial sums of this workgroup's tiles.
     float* part = a.part + (long long)blockIdx.x * 2 * a.C;
@@ -213,6 +229,7 @@ __global__ __launch_bounds__(1024) void k_block_reduce(BlockArgs a, int parts)
     const int lc = (int)threadIdx.x & 15, gr = (int)threadIdx.x >> 4, c = (int)blockIdx.x * 16 + lc;
     double q = 0.0, s = 0.0;
     if (c < a.C)
+#pragma unroll 4
         for (int p = gr; p < parts; p += 64) {
             const float* r = a.part + (long long)p * 2 * a.C;
             q += (double)r[c];
@@ -250,22 +267,37 @@ hipError_t run(const BlockArgs& a, const Shape& s, hipStream_t st)
 template <class T, bool JOIN>
 hipError_t dispatch(const BlockArgs& a, hipStream_t st)
 {
-    // The join holds five tensors: four elements a lane and workgroups of 1024
-    // threads keep two groups of channels within 128 registers on 128-byte rows
-    // (bf16; eight elements a lane spill: 2.0 against 2.5 ms at 2 x 128 x 1024^2).
-    constexpr int F = 16 / (int)sizeof(T), V = JOIN ? 4 : F, NT = JOIN ? 1024 : 512;
-    const Shape s = JOIN ? pick(a, V, NT, 2, 4) : pick(a, V, NT, 4, 8);
+    // The join holds five tensors: four elements a lane keep two groups of
+    // channels within 128 registers (bf16; eight elements a lane spill).  Workgroups
+    // of 1024 threads give rows of 128 bytes at 128 channels where there are many
+    // tiles (2.01 against 2.13 ms at 2 x 128 x 1024^2), of 512 threads twice the
+    // tiles where there are few (17 against 24 us at 3 x 100 x 37 x 53).
+    constexpr int F = 16 / (int)sizeof(T), V = JOIN ? 4 : F;
+    Shape s = JOIN ? pick(a, V, 1024, 2, 4) : pick(a, V, 512, 4, 8);
+    if (JOIN && !s.row && s.V > 1 && s.g.tiles < 2048 && a.C <= 2048) s = pick(a, V, 512, 2, 4);
     if (s.row) {
         if (s.K == 1) return run<T, JOIN, F, 1, true, 512>(a, s, st);
         if (s.K == 2) return run<T, JOIN, F, 2, true, 512>(a, s, st);
         return run<T, JOIN, F, 4, true, 512>(a, s, st);
     }
     if (s.V > 1) {
-        if (s.K == 1) return run<T, JOIN, V, 1, false, NT>(a, s, st);
-        if (s.K == 2) return run<T, JOIN, V, 2, false, NT>(a, s, st);
-        if (s.K == 4) return run<T, JOIN, V, 4, false, NT>(a, s, st);
-        if (JOIN || s.K == 8) return run<T, JOIN, V, 8, false, NT>(a, s, st);  // the join: 8192 channels at most
-        if constexpr (!JOIN) return run<T, JOIN, V / 2, 16, false, NT>(a, s, st);
+        if constexpr (JOIN) {
+            if (s.nt == 1024) {
+                if (s.K == 1) return run<T, JOIN, V, 1, false, 1024>(a, s, st);
+                if (s.K == 2) return run<T, JOIN, V, 2, false, 1024>(a, s, st);
+                if (s.K == 4) return run<T, JOIN, V, 4, false, 1024>(a, s, st);
+                return run<T, JOIN, V, 8, false, 1024>(a, s, st);  // 8192 channels at most
+            }
+            if (s.K == 1) return run<T, JOIN, V, 1, false, 512>(a, s, st);
+            if (s.K == 2) return run<T, JOIN, V, 2, false, 512>(a, s, st);
+            return run<T, JOIN, V, 4, false, 512>(a, s, st);  // 2048 channels at most
+        } else {
+            if (s.K == 1) return run<T, JOIN, V, 1, false, 512>(a, s, st);
+            if (s.K == 2) return run<T, JOIN, V, 2, false, 512>(a, s, st);
+            if (s.K == 4) return run<T, JOIN, V, 4, false, 512>(a, s, st);
+            if (s.K == 8) return run<T, JOIN, V, 8, false, 512>(a, s, st);
+            return run<T, JOIN, V / 2, 16, false, 512>(a, s, st);
+        }
     }
     if (s.K == 1) return run<T, JOIN, 1, 1, false, 512>(a, s, st);
     if (s.K == 2) return run<T, JOIN, 1, 2, false, 512>(a, s, st);
