@@ -23,6 +23,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import threading
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -147,14 +148,15 @@ def _call(device, stream, inputs, body):
 
 def _ws(workspace, kind, nbytes, device, st):
     """(buffer, bytes): the caller's workspace, or one of the cache, one per kind,
-    device, size and stream.  A captured call takes memory of its graph instead:
+    device, size, stream and host thread (the launches of two threads' calls may
+    interleave on one stream).  A captured call takes memory of its graph instead:
     a cached buffer would be shared with other graphs and with eager calls, which
     a replay does not wait for."""
     if workspace is not None:
         return workspace, _ws_bytes(workspace, device)
     if torch.cuda.is_current_stream_capturing():
         return torch.empty(max(nbytes, 8), dtype=torch.uint8, device=device), nbytes
-    key = (kind, device.index, nbytes, st)
+    key = (kind, device.index, nbytes, st, threading.get_ident())
     buf = _ws_cache.get(key)
     if buf is None:
         buf = _ws_cache[key] = torch.empty(max(nbytes, 8), dtype=torch.uint8, device=device)

@@ -28,7 +28,8 @@ ARCH = "gfx950"
 
 # Kernel translation units (one per group of chains, compiled in parallel) and
 # the C ABI.
-SOURCES = sorted(f for f in os.listdir(CSRC) if f.startswith("k_") and f.endswith(".hip")) + ["api.cpp", "api_block.cpp"]
+SOURCES = sorted(f for f in os.listdir(CSRC) if f.startswith("k_") and f.endswith(".hip")) + ["api.cpp",
+                                                                                              "api_block.cpp"]
 FLAGS = ["-std=c++20", "-O3", f"--offload-arch={ARCH}", "-fPIC",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
          "-I", os.path.join(ROOT, "include")]

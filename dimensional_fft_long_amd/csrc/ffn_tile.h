@@ -18,6 +18,14 @@
 //
 // Pipeline: NST LDS stages of BK terms, filled from global memory directly (16
 // bytes a lane) NST - 1 stages ahead; one barrier per stage.
+//
+// Measured on one MI355X at 1024 channels, 4096 hidden, 32768 positions, bf16:
+// 1.0 to 1.15 PFLOP/s (y 0.24 to 0.26 ms, both weight gradients of the hidden
+// layer 0.55 ms), half of the matrix cores' cycles at the 1.8 GHz that the card
+// holds under this load, no LDS bank conflicts; library products of that size
+// reach 1.27 to 1.52.  A tile reads 192 KB of fragments from LDS and takes 64 KB
+// of loads for each 2048 matrix cycles, which is all that LDS moves (124 bytes a
+// clock measured).
 #pragma once
 
 #include <type_traits>

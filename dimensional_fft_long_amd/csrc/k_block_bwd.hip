@@ -1,7 +1,7 @@
 // k_block_bwd.hip -- the norm and the join, backward.
 //
-// Measured on one MI355X: norm of 2 x 1024 x 16384 bf16 (three tensors) 97 us,
-// 2.1 TB/s; join of 2 x 128 x 1024^2 bf16 (eight tensors) 2.0 ms, 2.1 TB/s.  The
+// Measured on one MI355X: norm of 2 x 1024 x 16384 bf16 (three tensors) 81 us,
+// 2.5 TB/s; join of 2 x 128 x 1024^2 bf16 (eight tensors) 2.0 ms, 2.1 TB/s.  The
 // join issues 133 vector instructions an element (46% of the issue slots) and
 // its waves wait for 67% of their cycles: four waves a SIMD of 128 registers
 // are what the five tensors leave, with three sums (each behind two barriers)

@@ -576,6 +576,86 @@ def test_layer_with_the_convolution(H):
         assert float((p - q).abs().max() / q.abs().max()) <= 1e-4, name
 
 
+@pytest.mark.parametrize("pre", [True, False], ids=["with-next-norm", "alone"])
+def test_autograd_is_the_backward_call(H, pre):
+    """Every differentiable call gives its backward's gradients, with inputs
+    missing, gradients expanded or absent, and outputs unused."""
+    t = _tensors(F32, 2, 24, (5, 7), 40, seed=9)
+    x, m, gate, dout, dh, s, w1, w2, Wg, Wu, Wd, rng = t
+    w2 = w2 if pre else None
+    leaf = [v.clone().requires_grad_() if v is not None else None for v in (x, m, gate, s, w1, w2)]
+    kw = dict(gate_act="silu", p=0.3, rng=rng)
+    out, h = H.block_join(leaf[0], leaf[1], leaf[2], leaf[3], leaf[4], leaf[5], **kw)
+    assert (h is None) == (not pre)
+    (out * dout).sum().backward()                          # h unused
+    want = H.block_join_bwd(x, m, dout, None, gate, s, w1, w2, **kw)
+    for v, k in zip(leaf, ("dx", "dm", "dgate", "dscale", "dw_post", "dw_pre")):
+        if v is not None and (k != "dw_pre" or pre):
+            assert torch.equal(v.grad, want[k]), k
+    a = x.clone().requires_grad_()
+    H.block_join(a, m)[0].sum().backward()                 # an expanded gradient, every option absent
+    assert torch.equal(a.grad, torch.ones_like(a))
+    a, b = x.clone().requires_grad_(), w1.clone().requires_grad_()
+    H.block_norm(a, b).sum().backward()
+    da, db = H.block_norm_bwd(x, w1, torch.ones_like(x))
+    assert torch.equal(a.grad, da) and torch.equal(b.grad, db)
+    a = x.clone().requires_grad_()
+    H.dropout(a, 0.3, rng).sum().backward()
+    assert torch.equal(a.grad, H.dropout_bwd(torch.ones_like(x), 0.3, rng))
+    a = x.clone().requires_grad_()
+    H.dropout(a, 0.0, None).sum().backward()
+    assert torch.equal(a.grad, torch.ones_like(a))
+    ws = [v.clone().requires_grad_() for v in (x, Wg, Wu, Wd)]
+    H.gated_ffn(*ws, act="gelu").backward(dout)
+    for v, q in zip(ws, H.gated_ffn_bwd(x, Wg, Wu, Wd, dout, act="gelu")):
+        assert torch.equal(v.grad, q)
+
+
+def test_offsets_beyond_32_bits(H):
+    """Tensors of more than 2^31 elements (and bytes past 2^32): the last
+    positions of each result against the 64-bit reference of those positions
+    alone (they depend on no others; the parameter gradients, which do, are taken
+    from the call on the part)."""
+    n = (1 << 31) + 8 * 1001
+    x = torch.empty(n, dtype=BF16, device="cuda")
+    x.normal_(generator=gen(1))
+    rng = rng_words(5, 7)
+    y = H.dropout_fwd(x, 0.5, rng)
+    part = rng.clone()
+    part[1] += (n - 4096) // 4
+    assert torch.equal(y[-4096:], H.dropout_fwd(x[-4096:].clone(), 0.5, part))
+    del y
+    C, L = 136, 1 << 23
+    x = torch.empty(2, C, L, dtype=BF16, device="cuda")
+    x.normal_(generator=gen(2))
+    w = 1 + rand(gen(3), (C,), scale=0.1)
+
+    def end(t, k=64):
+        return t[1:, :, -k:].contiguous()
+
+    h = H.block_norm_fwd(x, w)
+    xt = end(x).double()
+    ref = xt * R.rms(xt, 1e-6) * R.ch(w.double(), xt)
+    check("h", end(h), ref, (R.HALF[BF16] + 2 * (C + 64) * U) * ref.abs())
+    out, _ = H.block_join_fwd(x, h, x, w, w)
+    g = H.block_join_bwd(x, h, x, None, x, w, w)
+    d = {"x": end(x), "m": end(h), "gate": end(x), "scale": w, "w_post": w, "w_pre": None}
+    gt = H.block_join_bwd(d["x"], d["m"], end(x), None, d["gate"], w, w)
+    gt.update({k: end(g[k]) for k in ("dx", "dm", "dgate")})
+    check_join(H, d, end(x), None, dict(gate_act="sigmoid", eps=1e-6, p=0.0), fwd=(end(out), None), bwd=gt)
+    del g, gt, out
+    for F, Cf in ((16, C), (40, 128)):                     # the tiles; one launch
+        xf = x[:, :Cf].contiguous() if Cf != C else x
+        Wg, Wu, Wd = (rand(gen(i), s, BF16, 0.1) for i, s in ((4, (F, Cf)), (5, (F, Cf)), (6, (Cf, F))))
+        y = H.gated_ffn_fwd(xf, Wg, Wu, Wd)
+        cut, dy = end(xf, 4096), end(xf, 4096)
+        bwd = list(H.gated_ffn_bwd(cut, Wg, Wu, Wd, dy))
+        if Cf == C:
+            bwd[0] = end(H.gated_ffn_bwd(xf, Wg, Wu, Wd, xf)[0], 4096)
+        check_ffn(H, cut, Wg, Wu, Wd, dy, "silu", fwd=end(y, 4096), bwd=bwd)
+    H.release_workspaces()
+
+
 def test_second_derivatives_are_refused(H):
     x = torch.ones(1, 3, 4, device="cuda", requires_grad=True)
     w = torch.ones(3, device="cuda", requires_grad=True)
