@@ -282,7 +282,8 @@ def _cached_ws(kind: str, nbytes: int, device, stream):
 
 
 def release_workspaces() -> None:
-    """Free the workspaces the calls above cached (one per shape and stream;
+    """Free the workspaces the calls above cached (one per shape and stream,
+    for the residual block's operators one per stream and host thread;
     a long-running program that meets many shapes calls this now and then).
     Each buffer's device is synchronised first, so no call in flight still
     uses it; the next call allocates afresh."""

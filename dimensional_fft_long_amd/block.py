@@ -148,17 +148,19 @@ def _call(device, stream, inputs, body):
 
 def _ws(workspace, kind, nbytes, device, st):
     """(buffer, bytes): the caller's workspace, or one of the cache, one per kind,
-    device, size, stream and host thread (the launches of two threads' calls may
-    interleave on one stream).  A captured call takes memory of its graph instead:
-    a cached buffer would be shared with other graphs and with eager calls, which
-    a replay does not wait for."""
+    device, stream and host thread (the launches of two threads' calls may
+    interleave on one stream), as large as its largest call.  A captured call
+    takes memory of its graph instead: a cached buffer would be shared with other
+    graphs and with eager calls, which a replay does not wait for."""
     if workspace is not None:
         return workspace, _ws_bytes(workspace, device)
     if torch.cuda.is_current_stream_capturing():
         return torch.empty(max(nbytes, 8), dtype=torch.uint8, device=device), nbytes
-    key = (kind, device.index, nbytes, st, threading.get_ident())
+    key = (kind, device.index, st, threading.get_ident())
     buf = _ws_cache.get(key)
-    if buf is None:
+    if buf is None or buf.numel() < nbytes:
+        _ws_cache.pop(key, None)
+        buf = None  # freed, in its stream's order, before the larger one is asked for
         buf = _ws_cache[key] = torch.empty(max(nbytes, 8), dtype=torch.uint8, device=device)
     return buf, nbytes
 
@@ -437,7 +439,10 @@ class GatedFFNFunction(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
-        dx, dWg, dWu, dWd = gated_ffn_bwd(*ctx.saved_tensors, dy.contiguous(), ctx.act)
+        dy = dy.contiguous()
+        if dy.data_ptr() % 16:  # part of a larger gradient
+            dy = dy.clone()
+        dx, dWg, dWu, dWd = gated_ffn_bwd(*ctx.saved_tensors, dy, ctx.act)
         return dx, dWg, dWu, dWd, None
 
 

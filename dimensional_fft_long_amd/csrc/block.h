@@ -52,7 +52,7 @@ struct FfnArgs {
     bool bf16;
 };
 
-// The one-launch forward for few channels (bf16, C <= kFusedMaxC): operands in
+// The one-launch forward for few channels (bf16, at most kFusedMaxC): operands in
 // rows of 16-byte multiples, x and y as in FfnArgs or packed.
 constexpr int kFusedMaxC = 128;
 struct FusedFfn {

@@ -107,8 +107,7 @@ __global__ __launch_bounds__(256) void k_ffn_sum(const float* part, int splits, 
 
 __global__ __launch_bounds__(256) void k_ffn_zero(unsigned short* p, long long n)
 {
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-    if (i < n) p[i] = 0;
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) p[i] = 0;
 }
 
 // Tiles.  bf16: Big fills a CU (128 KB of stages, eight waves); Mid runs two
@@ -363,6 +362,15 @@ struct Chain {
         a.goff = 1;
     }
 
+    // Few channels, and few hidden rows or many positions.  A workgroup of the
+    // one-launch form goes through all hidden rows by itself, 1.8 to 2.6 us a
+    // hundred, however few workgroups there are.  Measured, us, one launch
+    // against tiles at 32 (128) channels: 1024 positions, 256 hidden 12 (12) / 15 (15),
+    // 1024 hidden 20 (31) / 17 (18), 4096 hidden 71 (109) / 42 (43); 8192
+    // positions, 1024 hidden 21 (33) / 24 (27); 32768 positions, 1024 hidden
+    // 22 (37) / 58 (68), 4096 hidden 77 (131) / 216 (260).
+    bool one_launch() const { return f.bf16 && f.C <= kFusedMaxC && (f.F <= 512 || o.T >= 16384); }
+
     hipError_t forward()
     {
         Planes x, wg, wu, wd, h = planes(o.h, f.F, o.Tp);
@@ -373,7 +381,7 @@ struct Chain {
         weight(f.Wu, o.wu, f.F, f.C, &wu, &mw);
         weight(f.Wd, o.wd, f.C, f.F, &wd, &md);
         if ((e = run_packs()) != hipSuccess) return e;
-        if (f.bf16 && f.C <= kFusedMaxC)
+        if (one_launch())
             return launch_ffn_fused(FusedFfn{x.p, wg.p, wu.p, wd.p, f.y, mx.ld, mx.sb, mx.L, mw.ld, md.ld, f.C, f.F,
                                              (int)o.T, f.act, f.L, f.C * f.L, (int)f.L}, st);
         TileArgs a = base(f.F, o.T, f.C);
@@ -477,8 +485,9 @@ struct Chain {
 
 hipError_t launch_ffn_zero(void* p, long long bytes, hipStream_t st)
 {
-    const long long n = bytes / 2;
-    hipLaunchKernelGGL(k_ffn_zero, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, (unsigned short*)p, n);
+    // A launch holds fewer than 2^32 threads; the largest weights have more halves.
+    const long long n = bytes / 2, blocks = (n + 255) / 256;
+    hipLaunchKernelGGL(k_ffn_zero, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, st, (unsigned short*)p, n);
     return launch_status();
 }
 

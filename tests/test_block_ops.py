@@ -611,6 +611,77 @@ def test_autograd_is_the_backward_call(H, pre):
         assert torch.equal(v.grad, q)
 
 
+@pytest.mark.parametrize("C,F,T", [(24, 520, 100), (128, 1032, 200), (100, 513, 77), (64, 512, 200), (40, 520, 16384),
+                                   (128, 520, 16376)], ids=lambda v: str(v))
+def test_ffn_both_forms_for_few_channels(H, C, F, T):
+    """bf16 with at most 128 channels, on both sides of 512 hidden rows and 16384 positions."""
+    check_ffn(H, *ffn_case(BF16, 1, C, F, (T,)), "silu")
+
+
+def test_part_of_a_larger_gradient(H):
+    """A gradient that arrives as an odd slice of another, off a 16-byte address."""
+    x, Wg, Wu, Wd, _ = ffn_case(F32, 1, 3, 5, (7,))
+    d = rand(gen(5), (2, 3, 7))
+    ws = [t.clone().requires_grad_() for t in (x, Wg, Wu, Wd)]
+    both = torch.cat([torch.zeros_like(x), H.gated_ffn(*ws)])
+    both.backward(d)
+    assert d[1:].data_ptr() % 16
+    for v, q in zip(ws, H.gated_ffn_bwd(x, Wg, Wu, Wd, d[1:].clone())):
+        assert torch.equal(v.grad, q)
+
+
+def test_two_host_threads_on_one_stream(H):
+    """Calls of two threads interleave on a stream: each thread has its own workspaces."""
+    import threading
+    sets = [_tensors(seed=s, dtype=F32) for s in (5, 6)]
+    want = [_all_ops(H, t) for t in sets]
+    got, gate = [None, None], threading.Barrier(2)
+
+    def run(i):
+        gate.wait()
+        got[i] = [_all_ops(H, sets[i]) for _ in range(20)]
+
+    ts = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    torch.cuda.synchronize()
+    for w, reps in zip(want, got):
+        assert all(torch.equal(a, b) for r in reps for a, b in zip(w, r))
+
+
+def test_workspaces_grow_and_are_kept(H):
+    """Calls of growing and shrinking sizes share one workspace of the largest."""
+    H.release_workspaces()
+    for T in (70, 700, 90, 5000, 71):
+        case = ffn_case(F32, 1, 24, 40, (T,))
+        check_ffn(H, *case, "silu")
+    held = [b.numel() for k, b in H._ws_cache.items() if k[0] == "gated_ffn_bwd"]
+    assert held == [H.gated_ffn_bwd_workspace_bytes(1, 24, 40, (5000,), F32)]
+    H.release_workspaces()
+
+
+def test_weights_beyond_32_bits(H):
+    """Weights of more than 2^31 elements: all hidden rows zero but the last 64,
+    which alone then make the results; a sum over no positions clears as many."""
+    C, F, k = 65536, 32840, 64
+    x, Wg, Wu, Wd, dy = ffn_case(BF16, 1, C, k, (72,))
+    big = [torch.zeros(s, dtype=BF16, device="cuda") for s in ((F, C), (F, C), (C, F))]
+    big[0][-k:], big[1][-k:], big[2][:, -k:] = Wg, Wu, Wd
+    y = H.gated_ffn_fwd(x, *big)
+    dx, gg, gu, gd = H.gated_ffn_bwd(x, *big, dy)
+    check_ffn(H, x, Wg, Wu, Wd, dy, "silu", fwd=y, bwd=(dx, gg[-k:], gu[-k:], gd[:, -k:]))
+    few = x[:, :, :3].contiguous()
+    check_ffn(H, few, Wg, Wu, Wd, few, "silu", fwd=H.gated_ffn_fwd(few, *big))
+    for g in (gg, gu):
+        assert not bool(g[:-k].any())
+    del dx, gg, gu, gd, g
+    H.release_workspaces()
+    for g in H.gated_ffn_bwd(x[:0], *big, x[:0])[1:]:
+        assert not bool(g[-1].any()) and not bool(g[0].any())
+
+
 def test_offsets_beyond_32_bits(H):
     """Tensors of more than 2^31 elements (and bytes past 2^32): the last
     positions of each result against the 64-bit reference of those positions
