@@ -72,7 +72,7 @@ bool bad_opt(const void* p, size_t a) { return p && !aligned(p, a); }
 
 size_t parts_bytes(int B, int C, long long L)
 {
-    return B <= 0 || C <= 0 || L <= 0 ? 0 : (size_t)kBlockMaxParts * 2u * (size_t)C * sizeof(float);
+    return B <= 0 || C <= 0 || L <= 0 ? 0 : (size_t)block_parts(C) * 2u * (size_t)C * sizeof(float);
 }
 
 size_t part_workspace(int B, int C, int d, const int64_t* dims, int dtype)

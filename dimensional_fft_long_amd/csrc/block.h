@@ -35,7 +35,10 @@ struct BlockArgs {
 };
 
 constexpr int kBlockMaxC = 8192;      // channels of a norm or join (held in registers by one workgroup)
-constexpr int kBlockMaxParts = 1024;  // workgroups of a backward launch, at most
+// Workgroups of a backward launch, at most; up to eight channels may take
+// workgroups of a wave.
+constexpr int kFewChannels = 8;
+constexpr int block_parts(int C) { return C <= kFewChannels ? 4096 : 1024; }
 
 hipError_t launch_block_fwd(const BlockArgs& a, hipStream_t st);
 hipError_t launch_block_bwd(const BlockArgs& a, hipStream_t st);

@@ -229,7 +229,7 @@ __global__ __launch_bounds__(1024) void k_block_reduce(BlockArgs a, int parts)
     const int lc = (int)threadIdx.x & 15, gr = (int)threadIdx.x >> 4, c = (int)blockIdx.x * 16 + lc;
     double q = 0.0, s = 0.0;
     if (c < a.C)
-#pragma unroll 4
+#pragma unroll 8
         for (int p = gr; p < parts; p += 64) {
             const float* r = a.part + (long long)p * 2 * a.C;
             q += (double)r[c];
@@ -256,7 +256,7 @@ __global__ __launch_bounds__(1024) void k_block_reduce(BlockArgs a, int parts)
 template <class T, bool JOIN, int V, int K, bool ROW, int NT>
 hipError_t run(const BlockArgs& a, const Shape& s, hipStream_t st)
 {
-    const unsigned grid = (unsigned)(s.g.tiles < kBlockMaxParts ? s.g.tiles : kBlockMaxParts);
+    const unsigned grid = (unsigned)(s.g.tiles < block_parts(a.C) ? s.g.tiles : block_parts(a.C));
     hipLaunchKernelGGL((k_block_bwd<T, JOIN, V, K, ROW, NT>), dim3(grid), dim3(s.nt), 0, st, a, s.g);
     const hipError_t e = launch_status();
     if (e != hipSuccess || !(a.dscale || a.dw_post || a.dw_pre)) return e;
@@ -274,13 +274,16 @@ hipError_t dispatch(const BlockArgs& a, hipStream_t st)
     // tiles where there are few (17 against 24 us at 3 x 100 x 37 x 53).
     constexpr int F = 16 / (int)sizeof(T), V = JOIN ? 4 : F;
     Shape s = JOIN ? pick(a, V, 1024, 2, 4) : pick(a, V, 512, 4, 8);
-    if (JOIN && !s.row && s.V > 1 && s.g.tiles < 2048 && a.C <= 2048) s = pick(a, V, 512, 2, 4);
+    if (JOIN && !s.row && s.V > 1 && s.nt == 1024 && s.g.tiles < 2048 && a.C <= 2048) s = pick(a, V, 512, 2, 4);
     if (s.row) {
         if (s.K == 1) return run<T, JOIN, F, 1, true, 512>(a, s, st);
         if (s.K == 2) return run<T, JOIN, F, 2, true, 512>(a, s, st);
         return run<T, JOIN, F, 4, true, 512>(a, s, st);
     }
     if (s.V > 1) {
+        if (s.nt == 64) return run<T, JOIN, V, 1, false, 64>(a, s, st);
+        if (s.nt == 128) return run<T, JOIN, V, 1, false, 128>(a, s, st);
+        if (s.nt == 256) return run<T, JOIN, V, 1, false, 256>(a, s, st);
         if constexpr (JOIN) {
             if (s.nt == 1024) {
                 if (s.K == 1) return run<T, JOIN, V, 1, false, 1024>(a, s, st);

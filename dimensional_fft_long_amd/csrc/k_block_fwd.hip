@@ -11,15 +11,13 @@
 namespace hyenand {
 namespace {
 
-constexpr int kNT = 512;
-
 // Four waves a SIMD (128 registers) also where a few registers then spill: with
 // eight positions and four groups of channels a thread, the join of 2 x 128 x
 // 1024^2 bf16 takes 675 us so and 780 us with two waves.
-template <class T, bool JOIN, int V, int K, bool ROW>
-__global__ __launch_bounds__(kNT, V * K <= 32 ? 4 : 2) void k_block_fwd(BlockArgs a, Lay g)
+template <class T, bool JOIN, int V, int K, bool ROW, int NT>
+__global__ __launch_bounds__(NT, V * K <= 32 ? 4 : 2) void k_block_fwd(BlockArgs a, Lay g)
 {
-    __shared__ __align__(16) float red[2 * red_floats(kNT)];
+    __shared__ __align__(16) float red[2 * red_floats(NT)];
     int turn = 0;
     const float invC = 1.0f / (float)a.C;
     unsigned long long seed = 0, offs = 0;
@@ -72,7 +70,7 @@ __global__ __launch_bounds__(kNT, V * K <= 32 ? 4 : 2) void k_block_fwd(BlockArg
 #pragma unroll
                 for (int v = 0; v < V; ++v)
                     if (!ROW || w.mine(k, v)) rm[0][v] += mr[k].get(v) * mr[k].get(v);
-            sum_channels<1, V, ROW, kNT>(rm, red, turn, g.lxs);
+            sum_channels<1, V, ROW, NT>(rm, red, turn, g.lxs);
 #pragma unroll
             for (int v = 0; v < V; ++v) rm[0][v] = __builtin_amdgcn_rsqf(rm[0][v] * invC + a.eps);
         }
@@ -104,7 +102,7 @@ __global__ __launch_bounds__(kNT, V * K <= 32 ? 4 : 2) void k_block_fwd(BlockArg
 #pragma unroll
                 for (int v = 0; v < V; ++v)
                     if (!ROW || w.mine(k, v)) ro[0][v] += o[k][v] * o[k][v];
-            sum_channels<1, V, ROW, kNT>(ro, red, turn, g.lxs);
+            sum_channels<1, V, ROW, NT>(ro, red, turn, g.lxs);
 #pragma unroll
             for (int v = 0; v < V; ++v) ro[0][v] = __builtin_amdgcn_rsqf(ro[0][v] * invC + a.eps);
 #pragma unroll
@@ -117,12 +115,12 @@ __global__ __launch_bounds__(kNT, V * K <= 32 ? 4 : 2) void k_block_fwd(BlockArg
     }
 }
 
-template <class T, bool JOIN, int V, int K, bool ROW>
+template <class T, bool JOIN, int V, int K, bool ROW, int NT = 512>
 hipError_t run(const BlockArgs& a, const Shape& s, hipStream_t st)
 {
     const long long cap = 1ll << 30;
     const unsigned grid = (unsigned)(s.g.tiles < cap ? s.g.tiles : cap);
-    hipLaunchKernelGGL((k_block_fwd<T, JOIN, V, K, ROW>), dim3(grid), dim3(s.nt), 0, st, a, s.g);
+    hipLaunchKernelGGL((k_block_fwd<T, JOIN, V, K, ROW, NT>), dim3(grid), dim3(s.nt), 0, st, a, s.g);
     return launch_status();
 }
 
@@ -130,13 +128,16 @@ template <class T, bool JOIN>
 hipError_t dispatch(const BlockArgs& a, hipStream_t st)
 {
     constexpr int V = 16 / (int)sizeof(T);
-    const Shape s = pick(a, V, kNT, 4, 8);
+    const Shape s = pick(a, V, 512, 4, 8);
     if (s.row) {
         if (s.K == 1) return run<T, JOIN, V, 1, true>(a, s, st);
         if (s.K == 2) return run<T, JOIN, V, 2, true>(a, s, st);
         return run<T, JOIN, V, 4, true>(a, s, st);
     }
     if (s.V > 1) {
+        if (s.nt == 64) return run<T, JOIN, V, 1, false, 64>(a, s, st);
+        if (s.nt == 128) return run<T, JOIN, V, 1, false, 128>(a, s, st);
+        if (s.nt == 256) return run<T, JOIN, V, 1, false, 256>(a, s, st);
         if (s.K == 1) return run<T, JOIN, V, 1, false>(a, s, st);
         if (s.K == 2) return run<T, JOIN, V, 2, false>(a, s, st);
         if (s.K == 4) return run<T, JOIN, V, 4, false>(a, s, st);

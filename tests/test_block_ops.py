@@ -182,6 +182,17 @@ def test_norm_shapes(H, B, C, dims, dtype):
     check("dw", gw, dw, U * dw.abs() + k2 * sum_ch(dh.double().abs() * xd.abs() * r))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("B,C,dims", [(2, 1, (300001,)), (1, 2, (530000,)), (2, 3, (270001,)), (3, 4, (200002,)),
+                                      (1, 5, (601, 1000)), (2, 8, (262147,)), (1, 9, (530001,))], ids=lambda v: str(v))
+def test_few_channels_many_positions(H, B, C, dims, dtype):
+    """Workgroups of one to four waves."""
+    test_norm_shapes(H, B, C, dims, dtype)
+    p = 0.3 if C in (3, 8) else 0.0
+    d, dout, dh, kw = join_case(dtype, B, C, dims, act="silu", p=p)
+    check_join(H, d, dout, dh, kw, rng=rng_words() if p else None)
+
+
 def test_join_rows_of_zeros_and_large_values(H):
     """A position whose channels are all zero has the finite factor eps^(-1/2);
     a dropped element passes x through whatever the branch holds there."""
