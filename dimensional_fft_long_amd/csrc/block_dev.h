@@ -15,6 +15,30 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 inline hipError_t launch_status() { return hipGetLastError(); }
 
+typedef __attribute__((address_space(3))) void lds_void;
+
+// 16 bytes a lane from global memory to LDS at the wave-uniform address l plus
+// 16 times the lane.  In assembly because the compiler, which cannot tell the
+// stage being filled from the one being read, waits for the builtin's load
+// before the next LDS read.  The instruction has no destination register; it is
+// complete at wait_loads(), which comes before the barrier ahead of its use.
+__device__ __forceinline__ void to_lds(const void* g, unsigned l)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(l), "v"(g) : "memory");
+}
+
+// All but the newest N of this wave's loads are complete.
+template <int N = 0>
+__device__ __forceinline__ void wait_loads()
+{
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ unsigned lds_address(const void* p)
+{
+    return (unsigned)(unsigned long long)(lds_void*)p;
+}
+
 // V consecutive elements of type T (float or __bf16), kept as loaded (two bf16
 // a register).  A group need not be aligned beyond its element: gfx950's vector
 // memory instructions take any address, so a row that starts at an odd element

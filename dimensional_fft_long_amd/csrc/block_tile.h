@@ -16,7 +16,7 @@ namespace {
 
 constexpr int kMaxP = 256;  // positions of a tile, at most
 // Floats of a sum over a workgroup's waves: every wave's values and the joined ones.
-constexpr int red_floats(int NT) { return (NT / 64 + 1) * 2 * kMaxP; }
+constexpr int red_floats(int NT, int P = kMaxP) { return (NT / 64 + 1) * 2 * P; }
 
 // How a launch lays its threads over a tile.
 struct Lay {
@@ -35,7 +35,7 @@ struct Lay {
 // singly (142 against 149 us for the join of 8 x 64 x 256^2 fp32).
 struct Run {
     long long first, end, step;
-    __device__ Run(const Lay& g)
+    __device__ __forceinline__ Run(const Lay& g)
     {
         const unsigned x = blockIdx.x & 7u, n = gridDim.x;
         first = blockIdx.x;
@@ -85,11 +85,11 @@ __device__ __forceinline__ float sum_lanes(float a, int lxs)
 // the waves in order, and everyone reads the joined values.  `red` has two
 // parts used in turn: a part is written again only behind the barriers of the
 // sum in between.
-template <int N, int V, bool ROW, int NT>
+template <int N, int V, bool ROW, int NT, int MP = kMaxP>
 __device__ __forceinline__ void sum_channels(float (&s)[N][V], float* red, int& turn, int lxs)
 {
     const int t = (int)threadIdx.x, nw = (int)blockDim.x >> 6, w = t >> 6, lane = t & 63;
-    float* buf = red + turn * red_floats(NT);
+    float* buf = red + turn * red_floats(NT, MP);
     turn ^= 1;
     if constexpr (ROW) {
 #pragma unroll
@@ -122,7 +122,7 @@ __device__ __forceinline__ void sum_channels(float (&s)[N][V], float* red, int& 
                 for (int v = 0; v < V; ++v) buf[(w * N + n) * P + lx * V + v] = s[n][v];
         }
         __syncthreads();
-        float* tot = buf + NT / 64 * 2 * kMaxP;
+        float* tot = buf + NT / 64 * 2 * MP;
         for (int e = t; e < N * P; e += (int)blockDim.x) {
             float a = 0.0f;
             for (int i = 0; i < nw; ++i) a += buf[i * N * P + e];
@@ -148,7 +148,7 @@ struct Where {
     long long tile;   // the tile's part, the same for every thread
     long long kstep;  // from group to group
     int l0, skip, cy, step, C;
-    __device__ Where(const BlockArgs& a, const Lay& g)
+    __device__ __forceinline__ Where(const BlockArgs& a, const Lay& g)
     {
         const int t = (int)threadIdx.x;
         C = a.C;
@@ -165,7 +165,7 @@ struct Where {
             l0 = (t & ((1 << g.lxs) - 1)) * V;
         }
     }
-    __device__ void at(const BlockArgs& a, const Lay& g, long long i)
+    __device__ __forceinline__ void at(const BlockArgs& a, const Lay& g, long long i)
     {
         if constexpr (ROW) {
             tile = i * a.C;
@@ -181,20 +181,20 @@ struct Where {
             asm volatile("" : "+v"(lane));
         }
     }
-    __device__ bool live(int k) const { return cy + k * step < C && skip < V; }
-    __device__ bool all_live(int k) const { return (ROW ? (int)blockDim.x * V : step) * (k + 1) <= C; }
-    __device__ int chan(int k, int v) const
+    __device__ __forceinline__ bool live(int k) const { return cy + k * step < C && skip < V; }
+    __device__ __forceinline__ bool all_live(int k) const { return (ROW ? (int)blockDim.x * V : step) * (k + 1) <= C; }
+    __device__ __forceinline__ int chan(int k, int v) const
     {
         const int c = cy + k * step;
         return ROW ? (c + V <= C ? c : C - V) + v : c;
     }
-    __device__ long long off(int k) const
+    __device__ __forceinline__ long long off(int k) const
     {
         if constexpr (ROW) return tile + chan(k, 0);
         return lane + (tile + (all_live(k) || cy + k * step < C ? k * kstep : 0));
     }
     // ROW: whether element v of group k is this lane's to count.
-    __device__ bool mine(int k, int v) const
+    __device__ __forceinline__ bool mine(int k, int v) const
     {
         const int c = cy + k * step;
         return c + V <= C || (c < C && v >= c + V - C);
@@ -228,14 +228,14 @@ __device__ __forceinline__ void store_group(void* p, const Where<V, ROW>& w, int
 template <int V, int K, bool ROW>
 struct Params {
     float v[K][ROW ? V : 1];
-    __device__ void load(const float* p, const Where<V, ROW>& w, float dflt)
+    __device__ __forceinline__ void load(const float* p, const Where<V, ROW>& w, float dflt)
     {
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
             for (int i = 0; i < (ROW ? V : 1); ++i) v[k][i] = p && w.cy + k * w.step < w.C ? p[w.chan(k, i)] : dflt;
     }
-    __device__ float at(int k, int i) const { return v[k][ROW ? i : 0]; }
+    __device__ __forceinline__ float at(int k, int i) const { return v[k][ROW ? i : 0]; }
 };
 
 // How a launch is cut: V elements along positions per lane (rows: along
@@ -259,7 +259,7 @@ inline long long tile_count(const BlockArgs& a, int V, int lxs)
 // waves, so that every row of threads has one (norm of 8 x 1 x 6.6 million bf16
 // 577 -> 73 us, join of 7 x 2 x 9.2 million fp32 1638 -> 575).  A single
 // position per batch entry is a row of channels.
-inline Shape pick(const BlockArgs& a, int V, int nt, int good, int most)
+inline Shape pick(const BlockArgs& a, int V, int nt, int good, int most, int maxp = kMaxP)
 {
     const int es = a.bf16 ? 2 : 4, full = 16 / es;
     Shape s{};
@@ -275,7 +275,8 @@ inline Shape pick(const BlockArgs& a, int V, int nt, int good, int most)
     s.V = a.L >= V ? V : 1;
     s.nt = s.V > 1 ? nt : 512;
     const auto groups = [&](int lxs) { return (a.C + (s.nt >> lxs) - 1) / (s.nt >> lxs); };
-    const int top = s.V == 1 ? 6 : s.V == 8 ? 5 : 6;
+    int top = 6;
+    while (s.V > 1 && (s.V << top) > maxp) --top;
     const long long enough = s.nt == 1024 ? 256 : 512;
     if (s.V > 1 && a.C <= kFewChannels && tile_count(a, s.V, top) >= 4 * enough)
         while (s.nt > 64 && (s.nt >> (top + 1)) >= a.C) s.nt /= 2;

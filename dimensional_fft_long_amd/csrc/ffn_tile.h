@@ -87,36 +87,12 @@ struct TileCfg {
     static constexpr int NACC = NPL == 1 ? 1 : 2;  // accumulators: the leading pair's, the small pairs'
 };
 
-typedef __attribute__((address_space(3))) void lds_void;
-
-// 16 bytes a lane from global memory to LDS at the wave-uniform address l plus
-// 16 times the lane.  In assembly because the compiler, which cannot tell the
-// stage being filled from the one being read, waits for the builtin's load
-// before the next LDS read.  The instruction has no destination register; it is
-// complete at wait_loads(), which comes before the barrier ahead of its use.
-__device__ __forceinline__ void to_lds(const void* g, unsigned l)
-{
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(l), "v"(g) : "memory");
-}
-
-// All but the newest N of this wave's loads are complete.
-template <int N = 0>
-__device__ __forceinline__ void wait_loads()
-{
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-
 // Swizzle of the 16-byte pieces of a k-contiguous row: with rows of 64 (128,
 // 256) bytes, 16 rows of one piece then lie in 16 different bank groups.
 template <int PR>
 __device__ __forceinline__ int piece_swizzle(int row)
 {
     return PR == 16 ? row & 15 : PR == 8 ? (row >> 1) & 7 : (row >> 2) & 3;
-}
-
-__device__ __forceinline__ unsigned lds_address(const void* p)
-{
-    return (unsigned)(unsigned long long)(lds_void*)p;
 }
 
 // Column-contiguous tiles are [term][BN / 8 pieces]; a transposing read takes 64

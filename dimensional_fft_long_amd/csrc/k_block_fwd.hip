@@ -78,7 +78,7 @@ __global__ __launch_bounds__(NT, V * K <= 32 ? 4 : 2) void k_block_fwd(BlockArgs
 #pragma unroll
         for (int v = 0; v < V; ++v) ro[0][v] = 0.0f;
         if constexpr (JOIN) {
-            with_gate(a.gate != nullptr, a.act, [&](auto act) {
+            with_gate(a.gate != nullptr, a.act, [&](auto act) __attribute__((always_inline)) {
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
 #pragma unroll

@@ -193,6 +193,38 @@ def test_few_channels_many_positions(H, B, C, dims, dtype):
     check_join(H, d, dout, dh, kw, rng=rng_words() if p else None)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("B,C,dims", [(1, 283, (2, 10037)), (2, 264, (8200,)), (2, 717, (684,)), (1, 1000, (4099,)),
+                                      (2, 520, (9000,)), (1, 2048, (520,)), (1, 2048, (1037,)), (1, 1536, (8192,)),
+                                      (3, 1030, (23,)), (1, 700, (4, 8))], ids=lambda v: str(v))
+def test_join_many_channels(H, B, C, dims, dtype):
+    """The join's backward with its tensors in LDS: rows of whole 16-byte pieces
+    and others, several tiles a workgroup and less than one."""
+    p = 0.3 if B * C * math.prod(dims) < 2 ** 21 else 0.0
+    d, dout, dh, kw = join_case(dtype, B, C, dims, act=("sigmoid", "silu", "none")[C % 3], p=p)
+    rng = rng_words() if p else None
+    check_join(H, d, dout, dh, kw, rng=rng)
+    g = H.block_join_bwd(d["x"], d["m"], dout, dh, *[d[q] for q in ("gate", "scale", "w_post", "w_pre")], **kw, rng=rng)
+    buf = {}
+    for k, t in (("x", d["x"]), ("m", d["m"]), ("gate", d["gate"]), ("dh", dh)):   # one tensor at a time off its 16 bytes
+        buf[k] = torch.empty(t.numel() + 1, dtype=dtype, device="cuda")[1:].view(t.shape).copy_(t)
+    for k in buf:
+        a = {q: buf[q] if q == k else (dh if q == "dh" else d[q]) for q in buf}
+        r = H.block_join_bwd(a["x"], a["m"], dout, a["dh"], a["gate"], d["scale"], d["w_post"], d["w_pre"], **kw, rng=rng)
+        assert all(torch.equal(r[q], g[q]) for q in g), k
+
+
+@pytest.mark.parametrize("L", [2000, 2001])
+@pytest.mark.parametrize("gate,scale,post,pre", [(0, 0, 0, 0), (1, 0, 0, 0), (0, 1, 0, 1), (0, 0, 1, 0), (1, 0, 1, 1)])
+def test_join_parts_of_many_channels(H, gate, scale, post, pre, L):
+    for dtype in (F32, BF16):
+        d, dout, dh, kw = join_case(dtype, 1, 400, (L,), gate, scale, post, pre, act="silu", p=0.2)
+        check_join(H, d, dout, dh, kw, rng=rng_words(-7, 3))
+        if pre:
+            check_join(H, d, dout, None, kw, rng=rng_words(-7, 3))
+            check_join(H, d, None, dh, kw, rng=rng_words(-7, 3))
+
+
 def test_join_rows_of_zeros_and_large_values(H):
     """A position whose channels are all zero has the finite factor eps^(-1/2);
     a dropped element passes x through whatever the branch holds there."""
