@@ -13,9 +13,10 @@ namespace {
 
 // Four waves a SIMD (128 registers) also where a few registers then spill: with
 // eight positions and four groups of channels a thread, the join of 2 x 128 x
-// 1024^2 bf16 takes 675 us so and 780 us with two waves.
+// 1024^2 bf16 takes 675 us so and 780 us with two waves.  fp32 with eight groups
+// keeps two waves of 256 registers (717 channels by 131072: 962 -> 492 us).
 template <class T, bool JOIN, int V, int K, bool ROW, int NT>
-__global__ __launch_bounds__(NT, V * K <= 32 ? 4 : 2) void k_block_fwd(BlockArgs a, Lay g)
+__global__ __launch_bounds__(NT, V * K * (JOIN ? (int)sizeof(T) : 2) <= 64 ? 4 : 2) void k_block_fwd(BlockArgs a, Lay g)
 {
     __shared__ __align__(16) float red[2 * red_floats(NT)];
     int turn = 0;
